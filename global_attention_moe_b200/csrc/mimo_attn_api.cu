@@ -25,7 +25,11 @@
 #include "attn_decode_tc.cuh"
 #include "attn_bwd_simple.cuh"
 #include "attn_bwd_tc.cuh"
+#include "key_weights.cuh"
+#include "kv_evict.cuh"
 #include "neighbors.cuh"
+#include "rms_norm.cuh"
+#include "route_grouped.cuh"
 #include "rope_k_prepass.cuh"
 #include "params.cuh"
 
@@ -181,6 +185,21 @@ bool bwd_attributes_ready(int dev) {
                                           bwd::kSmemBytes) == cudaSuccess &&
                              cudaFuncSetAttribute(attn_bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   bwdtc::kSmemBytes) == cudaSuccess
+                         ? 1
+                         : -1);
+  return state[dev].load() == 1;
+}
+
+// The same for the key-weights kernels.
+bool key_weights_ready(int dev) {
+  static std::atomic<int> state[64];  // 0 unknown, 1 ready, -1 failed
+  if (dev < 0 || dev >= 64) return false;
+  if (state[dev].load() == 0)
+    state[dev].store(cudaFuncSetAttribute(kw::kw_main_kernel<2, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kw::kSmemBytes) == cudaSuccess &&
+                             cudaFuncSetAttribute(kw::kw_main_kernel<1, 2>,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  kw::kSmemBytes) == cudaSuccess
                          ? 1
                          : -1);
   return state[dev].load() == 1;
@@ -692,6 +711,139 @@ int launch_bwd(const void* q, const void* k, const void* v, const float* sink, c
   if (cudaFreeAsync(scratch, stream) != cudaSuccess) st = MIMO_ERR_CUDA;
   return st;
 }
+
+// ---------------------------------------------------------------- RMS norm
+bool norm_sizes_ok(int64_t features, bool codes, int& st) {
+  st = MIMO_OK;
+  if (features < 1) st = MIMO_ERR_INVALID_ARG;
+  else if (features % (codes ? 16 : 8) != 0 || features > rms::kMaxFeatures) st = MIMO_ERR_UNSUPPORTED;
+  return st == MIMO_OK;
+}
+
+template <int TPR, int V>
+void launch_norm(const rms::NormParams& P, bool w32, cudaStream_t stream) {
+  constexpr int threads = TPR < 128 ? 128 : TPR;
+  const unsigned grid = (unsigned)((P.T + threads / TPR - 1) / (threads / TPR));
+  if (P.codes != nullptr) {
+    if (w32)
+      rms::rms_norm_kernel<TPR, V, true, float><<<grid, threads, 0, stream>>>(P);
+    else
+      rms::rms_norm_kernel<TPR, V, true, uint16_t><<<grid, threads, 0, stream>>>(P);
+  } else {
+    if (w32)
+      rms::rms_norm_kernel<TPR, V, false, float><<<grid, threads, 0, stream>>>(P);
+    else
+      rms::rms_norm_kernel<TPR, V, false, uint16_t><<<grid, threads, 0, stream>>>(P);
+  }
+}
+
+// CTAs of the gradient kernel: one per SM at most (kMaxBwdCtas bounds the workspace), each walking rows.
+constexpr int64_t kMaxBwdCtas = 160;
+int norm_bwd_groups(int64_t features) {  // rows a CTA works on at a time
+  const int64_t n = features / 8;
+  return rms::kBwdThreads / (n <= 128 ? 32 : n <= 512 ? 128 : 512);
+}
+int64_t norm_bwd_ctas(int64_t tokens, int64_t features, int64_t most) {
+  const int g = norm_bwd_groups(features);
+  return std::min<int64_t>((tokens + g - 1) / g, most);
+}
+
+template <int TPR, int V>
+void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaStream_t stream) {
+  const size_t smem = TPR < rms::kBwdThreads ? (size_t)P.H * 4 : 0;  // the row groups' sums
+  if (w32)
+    rms::rms_norm_bwd_kernel<TPR, V, float><<<grid, rms::kBwdThreads, smem, stream>>>(P);
+  else
+    rms::rms_norm_bwd_kernel<TPR, V, uint16_t><<<grid, rms::kBwdThreads, smem, stream>>>(P);
+}
+
+// ---------------------------------------------------------------- key weights
+constexpr int64_t kSmsForSplits = 148;  // the split of the query tiles, which sizes the workspace, goes by this
+
+// Workspace layout (each part 256-byte aligned) and the split of the query tiles.
+struct KeyWeightsPlan {
+  int splits, ntile;
+  bool contiguous;
+  size_t qs, lse2, units, partial, bytes;
+};
+KeyWeightsPlan key_weights_plan(const mimo_decode_dims* d) {
+  KeyWeightsPlan p;
+  const int64_t group = d->num_q_heads / d->num_kv_heads;
+  const int64_t rows = std::max<int64_t>(1, (int64_t)d->max_q_len * group);
+  p.ntile = (int)(rows >= kw::kTile ? kw::kTile : (rows + 15) / 16 * 16);
+  const int64_t qtiles = (rows + p.ntile - 1) / p.ntile;
+  p.contiguous = qtiles == 1;
+  // enough units for about four per SM
+  const int64_t units = ((int64_t)d->total_kv / kw::kTile + d->num_seqs) * d->num_kv_heads;
+  p.splits = (int)std::max<int64_t>(
+      1, std::min({qtiles, (int64_t)kw::kMaxSplits, (4 * kSmsForSplits + units - 1) / units}));
+  const size_t qrows = (size_t)d->total_q * d->num_q_heads;
+  p.qs = 0;
+  p.lse2 = p.qs + align256(qrows * 512);
+  p.units = p.lse2 + align256(qrows * 4);
+  p.partial = p.units + align256(((size_t)d->num_seqs + 1) * 8);
+  p.bytes = p.partial + align256((size_t)p.splits * d->num_kv_heads * d->total_kv * 4);
+  return p;
+}
+
+int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const int32_t* indptr, const int32_t* cu_q,
+                       const float* lse, const float* prev, const mimo_decode_dims* d, int layer_kind, int window,
+                       double rope_base, float* out, void* workspace, cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MIMO_ERR_CUDA;
+  DeviceInfo* info = device_info(dev);
+  if (!info || !key_weights_ready(dev)) return MIMO_ERR_CUDA;
+  const KeyWeightsPlan plan = key_weights_plan(d);
+  char* ws = static_cast<char*>(workspace);
+  kw::Params P;
+  std::memset(&P, 0, sizeof P);
+  P.q = static_cast<const uint16_t*>(q);
+  P.k_cache = static_cast<const uint16_t*>(kc);
+  P.kv_indices = idx;
+  P.kv_indptr = indptr;
+  P.cu_q = cu_q;
+  P.lse = lse;
+  P.prev = prev;
+  P.out = out;
+  P.qs = reinterpret_cast<uint16_t*>(ws + plan.qs);
+  P.lse2 = reinterpret_cast<float*>(ws + plan.lse2);
+  P.units = reinterpret_cast<long long*>(ws + plan.units);
+  P.partial = reinterpret_cast<float*>(ws + plan.partial);
+  P.num_seqs = d->num_seqs;
+  P.total_q = d->total_q;
+  P.total_kv = d->total_kv;
+  P.cache_rows = d->cache_rows;
+  P.max_q_len = d->max_q_len;
+  P.max_kv_len = d->max_kv_len;
+  P.hq = d->num_q_heads;
+  P.hkv = d->num_kv_heads;
+  P.group = d->num_q_heads / d->num_kv_heads;
+  P.window = (layer_kind == MIMO_LAYER_GLOBAL) ? -1 : window;
+  P.splits = plan.splits;
+  P.ntile = plan.ntile;
+  P.contiguous = plan.contiguous ? 1 : 0;
+  P.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDimQK)));
+  P.wait_limit_ns = kDefaultWaitLimitNs;
+  for (int i = 0; i < kRopeDims / 2; ++i) P.theta[i] = std::pow(rope_base, -2.0 * i / kRopeDims);
+  const long long warps = (long long)d->total_q * ((P.hq + kw::kPrepHeads - 1) / kw::kPrepHeads);
+  const unsigned prep_grid = (unsigned)((warps + kw::kPrepThreads / 32 - 1) / (kw::kPrepThreads / 32) + 1);
+  kw::kw_prep_kernel<<<prep_grid, kw::kPrepThreads, 0, stream>>>(P);
+  if (cudaGetLastError() != cudaSuccess) return MIMO_ERR_CUDA;
+  if (d->total_q > 0) {
+    CUtensorMap tq;
+    if (!encode_2d(&tq, P.qs, 256, (uint64_t)d->total_q * P.hq, (uint32_t)P.ntile)) return MIMO_ERR_CUDA;
+    const long long units = ((long long)d->total_kv / kw::kTile + d->num_seqs) * P.hkv * P.splits;
+    const unsigned grid = (unsigned)std::min<long long>(units, info->sms);
+    if (P.contiguous)
+      kw::kw_main_kernel<2, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+    else
+      kw::kw_main_kernel<1, 2><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+    if (cudaGetLastError() != cudaSuccess) return MIMO_ERR_CUDA;
+  }
+  kw::kw_join_kernel<<<(unsigned)(((long long)d->total_kv + kw::kJoinThreads - 1) / kw::kJoinThreads),
+                       kw::kJoinThreads, 0, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
 }  // namespace
 
 extern "C" {
@@ -960,7 +1112,217 @@ int mimo_moe_route(const float* logits, const float* bias, int64_t tokens, int n
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 
-int mimo_attn_version(void) { return (1 << 16) | 5; }
+int mimo_rms_norm(const void* x, const void* residual, const void* weight, int weight_fp32, int64_t tokens,
+                  int64_t features, float eps, void* h, void* y, void* codes, float* scale_inv, void* stream) {
+  int st;
+  if (tokens < 0 || !(eps >= 1e-18f && eps <= 1e18f)) return MIMO_ERR_INVALID_ARG;
+  if (!norm_sizes_ok(features, codes != nullptr, st)) return st;
+  if (tokens > INT32_MAX) return MIMO_ERR_UNSUPPORTED;
+  if (tokens == 0) return MIMO_OK;
+  if (!x || !weight || (!y && !codes) || (codes && !scale_inv)) return MIMO_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, weight, (const void*)h, (const void*)y, (const void*)codes})
+    if (!aligned16(p)) return MIMO_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(scale_inv) & 3u) return MIMO_ERR_INVALID_ARG;
+  rms::NormParams P;
+  P.x = static_cast<const uint16_t*>(x);
+  P.r = static_cast<const uint16_t*>(residual);
+  P.w = weight;
+  P.h = static_cast<uint16_t*>(h);
+  P.y = static_cast<uint16_t*>(y);
+  P.codes = static_cast<uint8_t*>(codes);
+  P.scale = scale_inv;
+  P.T = tokens;
+  P.H = (int)features;
+  P.eps = eps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool w32 = weight_fp32 != 0;
+  const int n = (int)features / 8;
+  if (n <= 32) launch_norm<32, 1>(P, w32, s);
+  else if (n <= 64) launch_norm<32, 2>(P, w32, s);
+  else if (n <= 128) launch_norm<32, 4>(P, w32, s);
+  else if (n <= 256) launch_norm<128, 2>(P, w32, s);
+  else if (n <= 512) launch_norm<128, 4>(P, w32, s);
+  else if (n <= 1024) launch_norm<512, 2>(P, w32, s);
+  else launch_norm<512, 4>(P, w32, s);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+size_t mimo_rms_norm_bwd_workspace_size(int64_t tokens, int64_t features) {
+  int st;
+  if (tokens < 0 || !norm_sizes_ok(features, false, st)) return 0;
+  return (size_t)norm_bwd_ctas(std::max<int64_t>(tokens, 1), features, kMaxBwdCtas) * (size_t)features * 4;
+}
+
+int mimo_rms_norm_bwd(const void* h, const void* weight, int weight_fp32, const void* dy, const void* dh,
+                      int64_t tokens, int64_t features, float eps, void* dx, float* dweight, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int st;
+  if (tokens < 0 || !(eps >= 1e-18f && eps <= 1e18f)) return MIMO_ERR_INVALID_ARG;
+  if (!norm_sizes_ok(features, false, st)) return st;
+  if (!dweight || !aligned16(dweight)) return MIMO_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tokens == 0)
+    return cudaMemsetAsync(dweight, 0, (size_t)features * 4, s) == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+  if (!h || !weight || !dy || !dx || !workspace) return MIMO_ERR_INVALID_ARG;
+  for (const void* p : {h, weight, dy, dh, (const void*)dx, (const void*)workspace})
+    if (!aligned16(p)) return MIMO_ERR_INVALID_ARG;
+  if (workspace_bytes < mimo_rms_norm_bwd_workspace_size(tokens, features)) return MIMO_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MIMO_ERR_CUDA;
+  DeviceInfo* info = device_info(dev);
+  if (!info) return MIMO_ERR_CUDA;
+  rms::NormBwdParams P;
+  P.h = static_cast<const uint16_t*>(h);
+  P.dy = static_cast<const uint16_t*>(dy);
+  P.dh = static_cast<const uint16_t*>(dh);
+  P.w = weight;
+  P.dx = static_cast<uint16_t*>(dx);
+  P.partial = static_cast<float*>(workspace);
+  P.T = tokens;
+  P.H = (int)features;
+  P.eps = eps;
+  const unsigned grid = (unsigned)norm_bwd_ctas(tokens, features, std::min<int64_t>(info->sms, kMaxBwdCtas));
+  const bool w32 = weight_fp32 != 0;
+  const int n = (int)features / 8;
+  if (n <= 32) launch_norm_bwd<32, 1>(P, w32, grid, s);
+  else if (n <= 64) launch_norm_bwd<32, 2>(P, w32, grid, s);
+  else if (n <= 128) launch_norm_bwd<32, 4>(P, w32, grid, s);
+  else if (n <= 256) launch_norm_bwd<128, 2>(P, w32, grid, s);
+  else if (n <= 512) launch_norm_bwd<128, 4>(P, w32, grid, s);
+  else if (n <= 1024) launch_norm_bwd<512, 2>(P, w32, grid, s);
+  else launch_norm_bwd<512, 4>(P, w32, grid, s);
+  if (cudaGetLastError() != cudaSuccess) return MIMO_ERR_CUDA;
+  const unsigned dw_grid = (unsigned)((features + 63) / 64);
+  rms::rms_norm_dw_kernel<<<dw_grid, rms::kDwThreads, 0, s>>>(P.partial, dweight, (int)grid, (int)features);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+int mimo_moe_route_grouped(const float* logits, const float* bias, int64_t tokens, int num_experts, int top_k,
+                           int num_groups, int top_groups, int score, int normalize, float scale, int32_t* ids,
+                           float* weights, void* stream) {
+  if (tokens < 0 || num_experts < 1 || top_k < 1 || num_groups < 1 || top_groups < 1 || top_groups > num_groups ||
+      num_experts % num_groups != 0 || top_k > (int64_t)top_groups * (num_experts / num_groups) ||
+      (score != MIMO_ROUTE_SIGMOID && score != MIMO_ROUTE_SOFTMAX) || !std::isfinite(scale))
+    return MIMO_ERR_INVALID_ARG;
+  if (num_experts > rg::kMaxExperts || top_k > 32 || num_groups > rg::kMaxGroups) return MIMO_ERR_UNSUPPORTED;
+  if (tokens == 0) return MIMO_OK;
+  if (!logits || !ids || !weights || !aligned16(logits) || !aligned16(bias) ||
+      ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(weights)) & 3u))
+    return MIMO_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MIMO_ERR_CUDA;
+  DeviceInfo* info = device_info(dev);
+  if (!info) return MIMO_ERR_CUDA;
+  rg::RouteParams P;
+  P.logits = logits;
+  P.bias = bias;
+  P.ids = ids;
+  P.weights = weights;
+  P.T = tokens;
+  P.E = num_experts;
+  P.top_k = top_k;
+  P.groups = num_groups;
+  P.top_groups = top_groups;
+  P.softmax = score == MIMO_ROUTE_SOFTMAX;
+  P.normalize = normalize != 0;
+  P.scale = scale;
+  const unsigned grid = (unsigned)std::min<long long>((tokens + rg::kWarps - 1) / rg::kWarps, 16LL * info->sms);
+  const size_t smem = (size_t)rg::kWarps * num_experts * 4;
+  rg::route_grouped_kernel<<<grid, rg::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const float* dweights, int64_t tokens,
+                       int num_experts, int top_k, int score, int normalize, float scale, float* dlogits,
+                       void* stream) {
+  if (tokens < 0 || num_experts < 1 || top_k < 1 || (score != MIMO_ROUTE_SIGMOID && score != MIMO_ROUTE_SOFTMAX) ||
+      !std::isfinite(scale))
+    return MIMO_ERR_INVALID_ARG;
+  if (num_experts > rg::kMaxExperts || top_k > 32) return MIMO_ERR_UNSUPPORTED;
+  if (tokens == 0) return MIMO_OK;
+  if (!logits || !ids || !dweights || !dlogits || !aligned16(logits) || !aligned16(dlogits) ||
+      ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(dweights)) & 3u))
+    return MIMO_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MIMO_ERR_CUDA;
+  DeviceInfo* info = device_info(dev);
+  if (!info) return MIMO_ERR_CUDA;
+  rg::RouteBwdParams P;
+  P.logits = logits;
+  P.ids = ids;
+  P.dweights = dweights;
+  P.dlogits = dlogits;
+  P.T = tokens;
+  P.E = num_experts;
+  P.top_k = top_k;
+  P.softmax = score == MIMO_ROUTE_SOFTMAX;
+  P.normalize = normalize != 0;
+  P.scale = scale;
+  const unsigned grid = (unsigned)std::min<long long>((tokens + rg::kWarps - 1) / rg::kWarps, 16LL * info->sms);
+  const size_t smem = (size_t)rg::kWarps * num_experts * 4;
+  rg::route_bwd_kernel<<<grid, rg::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+size_t mimo_decode_key_weights_workspace_size(const mimo_decode_dims* d) {
+  // the sizes alone: any aligned address stands for the buffers
+  const void* p = reinterpret_cast<const void*>(uintptr_t(256));
+  const int32_t* i = static_cast<const int32_t*>(p);
+  if (validate_decode(p, p, p, i, i, i, nullptr, d, MIMO_LAYER_GLOBAL, -1, 1e4, kRopeDims, 1.f, p,
+                      static_cast<const float*>(p)) != MIMO_OK)
+    return 0;
+  return key_weights_plan(d).bytes;
+}
+
+int mimo_decode_key_weights(const void* q, const void* k_cache, const int32_t* kv_indices, const int32_t* kv_indptr,
+                            const int32_t* cu_q, const float* lse, const float* prev, const mimo_decode_dims* dims,
+                            int layer_kind, int window, double rope_base, int rope_dims, float* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  // the checks of the KV-cache attention; there is no V and no output row here (any aligned address passes)
+  const void* none = reinterpret_cast<const void*>(uintptr_t(256));
+  int st = validate_decode(q, k_cache, none, kv_indices, kv_indptr, cu_q, nullptr, dims, layer_kind, window, rope_base,
+                           rope_dims, 1.f, none, lse);
+  if (st != MIMO_OK) return st;
+  if ((int64_t)dims->total_q * dims->num_q_heads > INT32_MAX) return MIMO_ERR_UNSUPPORTED;  // rows of a tensor map
+  if (dims->total_kv == 0) return MIMO_OK;
+  if (!out || !workspace || ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(prev)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < key_weights_plan(dims).bytes)
+    return MIMO_ERR_INVALID_ARG;
+  return launch_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, prev, dims, layer_kind, window, rope_base,
+                            out, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int mimo_kv_evict(const float* weights, const int32_t* kv_indices, const int32_t* kv_indptr, int num_seqs,
+                  int total_kv, int max_kv_len, int budget, int keep_first, int keep_recent, int32_t* new_indices,
+                  float* new_weights, int32_t* new_indptr, int32_t* freed, void* stream) {
+  if (num_seqs < 1 || total_kv < 0 || max_kv_len < 0 || max_kv_len > total_kv || keep_first < 0 || keep_recent < 0 ||
+      (int64_t)keep_first + keep_recent > budget)
+    return MIMO_ERR_INVALID_ARG;
+  if (!kv_indptr || !new_indptr) return MIMO_ERR_INVALID_ARG;
+  if (total_kv > 0 && (!weights || !kv_indices || !new_indices || !new_weights || !freed)) return MIMO_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)weights, (const void*)kv_indices, (const void*)kv_indptr,
+                        (const void*)new_indices, (const void*)new_weights, (const void*)new_indptr,
+                        (const void*)freed})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return MIMO_ERR_INVALID_ARG;
+  ev::EvictParams P;
+  P.weights = weights;
+  P.kv_indices = kv_indices;
+  P.kv_indptr = kv_indptr;
+  P.new_indices = new_indices;
+  P.new_weights = new_weights;
+  P.new_indptr = new_indptr;
+  P.freed = freed;
+  P.num_seqs = num_seqs;
+  P.total_kv = total_kv;
+  P.max_kv_len = max_kv_len;
+  P.budget = budget;
+  P.first = keep_first;
+  P.recent = keep_recent;
+  ev::kv_evict_kernel<<<(unsigned)num_seqs, ev::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+int mimo_attn_version(void) { return (1 << 16) | 6; }
 
 int mimo_attn_fwd_noalloc(const void* q, const void* k, const void* v, const float* sink,
                           const int32_t* cu_seqlens, const mimo_attn_dims* dims, int layer_kind, int window,

@@ -23,7 +23,9 @@ SYMBOLS = ("mimo_attn_fwd", "mimo_attn_host_workspace_size", "mimo_attn_fwd_host
            "mimo_attn_noalloc_scratch_bytes", "mimo_attn_set_kernel", "mimo_attn_profile_start",
            "mimo_attn_profile_stop", "mimo_attn_profile_set_stride", "mimo_attn_decode", "mimo_attn_set_decode_kernel", "mimo_attn_version",
            "mimo_attn_bwd", "mimo_fp8_dequant_blockwise", "mimo_qkv_split", "mimo_moe_route",
-           "mimo_linear_proj", "mimo_attn_set_bwd_kernel")
+           "mimo_linear_proj", "mimo_attn_set_bwd_kernel", "mimo_rms_norm", "mimo_rms_norm_bwd",
+           "mimo_rms_norm_bwd_workspace_size", "mimo_moe_route_grouped", "mimo_moe_route_bwd",
+           "mimo_decode_key_weights", "mimo_decode_key_weights_workspace_size", "mimo_kv_evict")
 KERNEL_AUTO, KERNEL_SIMPLE, KERNEL_PIPELINED, KERNEL_WINDOW, KERNEL_WINDOW_PACKED = 0, 1, 2, 3, 4
 DECODE_AUTO, DECODE_CUDA_CORES, DECODE_TENSOR = 0, 1, 2
 
@@ -92,6 +94,23 @@ def _load():
     lib.mimo_linear_proj.argtypes = [P, P, L, L, L, P, P]
     lib.mimo_moe_route.restype = I
     lib.mimo_moe_route.argtypes = [P, P, L, I, I, I, P, P, P]
+    lib.mimo_rms_norm.restype = I
+    lib.mimo_rms_norm.argtypes = [P, P, P, I, L, L, F, P, P, P, P, P]
+    lib.mimo_rms_norm_bwd.restype = I
+    lib.mimo_rms_norm_bwd.argtypes = [P, P, I, P, P, L, L, F, P, P, P, ctypes.c_size_t, P]
+    lib.mimo_rms_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.mimo_rms_norm_bwd_workspace_size.argtypes = [L, L]
+    lib.mimo_moe_route_grouped.restype = I
+    lib.mimo_moe_route_grouped.argtypes = [P, P, L, I, I, I, I, I, I, F, P, P, P]
+    lib.mimo_moe_route_bwd.restype = I
+    lib.mimo_moe_route_bwd.argtypes = [P, P, P, L, I, I, I, I, F, P, P]
+    lib.mimo_decode_key_weights.restype = I
+    lib.mimo_decode_key_weights.argtypes = [P, P, P, P, P, P, P, ctypes.POINTER(DecodeDims), I, I, D, I, P, P,
+                                            ctypes.c_size_t, P]
+    lib.mimo_decode_key_weights_workspace_size.restype = ctypes.c_size_t
+    lib.mimo_decode_key_weights_workspace_size.argtypes = [ctypes.POINTER(DecodeDims)]
+    lib.mimo_kv_evict.restype = I
+    lib.mimo_kv_evict.argtypes = [P, P, P, I, I, I, I, I, I, P, P, P, P, P]
     lib.mimo_attn_set_decode_kernel.restype = I
     lib.mimo_attn_set_decode_kernel.argtypes = [I]
     lib.mimo_attn_version.restype = I
@@ -361,3 +380,189 @@ def decode(q, k_cache, v_cache, kv_indices, kv_indptr, cu_q, sink, max_q_len, ma
     if st != OK:
         raise MimoAttnError(st, "mimo_attn_decode")
     return out, lse
+
+
+def _check_tensors(*specs):
+    """Each spec: (name, tensor, dtypes, shape); None tensors pass.  Contiguous CUDA tensors of the current
+    device only: kernels are launched there, and rows are read as one dense block."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t, dtypes, shape in specs:
+        if t is None:
+            continue
+        if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} with shape "
+                             f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+        if t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _on(stream):
+    """Outputs and workspaces are allocated on the stream the kernels run on, so that memory another stream
+    still uses is never handed out."""
+    import contextlib
+
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _norm(x, weight, residual, eps, with_y, with_fp8, stream):
+    import torch
+    bf16 = (torch.bfloat16,)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [tokens, features], got {tuple(x.shape)}")
+    T, H = x.shape
+    _check_tensors(("x", x, bf16, x.shape), ("weight", weight, (torch.bfloat16, torch.float32), (H,)),
+                   ("residual", residual, bf16, x.shape))
+    y = h = codes = scale = None
+    with _on(stream):
+        if residual is not None:
+            h = torch.empty_like(x)
+        if with_y:
+            y = torch.empty_like(x)
+        if with_fp8:
+            codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+            scale = torch.empty((T, (H + 127) // 128), dtype=torch.float32, device=x.device)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    st = LIB.mimo_rms_norm(x.data_ptr(), ptr(residual), weight.data_ptr(), int(weight.dtype == torch.float32), T, H,
+                           float(eps), ptr(h), ptr(y), ptr(codes), ptr(scale), _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_rms_norm")
+    return y, codes, scale, x if h is None else h
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
+    """RMS norm of x (+ residual): bf16 x / residual [T, H] (CUDA), weight [H] bf16 or fp32.  Returns (y bf16
+    [T, H], h bf16 [T, H]); h = bf16(x + residual) is the new residual stream (x itself without a residual)."""
+    y, _, _, h = _norm(x, weight, residual, eps, True, False, stream)
+    return y, h
+
+
+def rms_norm_fp8(x, weight, residual=None, eps=1e-6, with_bf16=False, stream=None):
+    """The same with y as E4M3 bytes and one scale per 1 x 128 block (fp8_dequant_blockwise(codes, scale_inv,
+    (1, 128)) gives it back).  Returns (codes uint8 [T, H], scale_inv fp32 [T, ceil(H/128)], h), and y in bf16
+    as a fourth with with_bf16."""
+    y, codes, scale, h = _norm(x, weight, residual, eps, bool(with_bf16), True, stream)
+    return (codes, scale, h, y) if with_bf16 else (codes, scale, h)
+
+
+def rms_norm_bwd(h, weight, dy, dh=None, eps=1e-6, stream=None):
+    """Gradients of rms_norm: h as it returned it (bf16 [T, H]), dy = dL/dy and dh = dL/dh by h's other uses
+    (None: 0), bf16.  Returns (dx bf16 [T, H], the gradient of x and of the residual; dweight fp32 [H])."""
+    import torch
+    bf16 = (torch.bfloat16,)
+    if h.dim() != 2:
+        raise ValueError(f"h must be [tokens, features], got {tuple(h.shape)}")
+    T, H = h.shape
+    _check_tensors(("h", h, bf16, h.shape), ("weight", weight, (torch.bfloat16, torch.float32), (H,)),
+                   ("dy", dy, bf16, h.shape), ("dh", dh, bf16, h.shape))
+    nbytes = LIB.mimo_rms_norm_bwd_workspace_size(T, H)
+    with _on(stream):
+        dx = torch.empty_like(h)
+        dw = torch.empty((H,), dtype=torch.float32, device=h.device)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=h.device)
+    st = LIB.mimo_rms_norm_bwd(h.data_ptr(), weight.data_ptr(), int(weight.dtype == torch.float32), dy.data_ptr(),
+                               None if dh is None else dh.data_ptr(), T, H, float(eps), dx.data_ptr(), dw.data_ptr(),
+                               ws.data_ptr(), nbytes, _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_rms_norm_bwd")
+    return dx, dw
+
+
+ROUTE_SIGMOID, ROUTE_SOFTMAX = 0, 1
+
+
+def moe_route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, score=ROUTE_SIGMOID, normalize=True,
+                      scale=1.0, stream=None):
+    """Routing with sigmoid or softmax scores, limited to the top_groups best of num_groups expert groups (a
+    group's score: the sum of its two largest score + bias).  fp32 logits [T, E] and bias [E] or None (CUDA) ->
+    ids int32 [T, top_k], weights fp32 [T, top_k] (scale times the scores, normalised to sum to one first)."""
+    import torch
+    f32 = (torch.float32,)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _check_tensors(("logits", logits, f32, logits.shape), ("bias", bias, f32, (E,)))
+    with _on(stream):
+        ids = torch.empty((T, max(int(top_k), 0)), dtype=torch.int32, device=logits.device)
+        w = torch.empty((T, max(int(top_k), 0)), dtype=torch.float32, device=logits.device)
+    st = LIB.mimo_moe_route_grouped(logits.data_ptr(), None if bias is None else bias.data_ptr(), T, E, int(top_k),
+                                    int(num_groups), int(top_groups), int(score), int(bool(normalize)), float(scale),
+                                    ids.data_ptr(), w.data_ptr(), _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_moe_route_grouped")
+    return ids, w
+
+
+def moe_route_bwd(logits, ids, dweights, score=ROUTE_SIGMOID, normalize=True, scale=1.0, stream=None):
+    """Gradient of moe_route_grouped's weights (or, with the defaults, moe_route's) with respect to the logits:
+    fp32 logits [T, E], int32 ids and fp32 dweights [T, top_k] (CUDA) -> dlogits fp32 [T, E].  An id outside
+    [0, E) is an empty place."""
+    import torch
+    f32 = (torch.float32,)
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError(f"logits and ids must be [tokens, ...], got {tuple(logits.shape)} and {tuple(ids.shape)}")
+    T, E = logits.shape
+    k = ids.shape[1]
+    _check_tensors(("logits", logits, f32, logits.shape), ("ids", ids, (torch.int32,), (T, k)),
+                   ("dweights", dweights, f32, (T, k)))
+    with _on(stream):
+        d = torch.empty_like(logits)
+    st = LIB.mimo_moe_route_bwd(logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), T, E, k, int(score),
+                                int(bool(normalize)), float(scale), d.data_ptr(), _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_moe_route_bwd")
+    return d
+
+
+def decode_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, max_q_len, max_kv_len, layer_kind, window,
+                       rope_base, rope_dims=64, prev=None, out=None, stream=None):
+    """Attention weight each cached key receives from a decode() step's new queries, summed over the query heads
+    and the sequence's queries: arguments as decode (lse fp32 [Hq, Tq] as it returned it), prev fp32 [total_kv]
+    or None is added.  Returns fp32 [total_kv], beside kv_indices (out, which may be prev, if given)."""
+    import torch
+    bf16, i32, f32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
+    if q.dim() != 3 or k_cache.dim() != 3:
+        raise ValueError(f"q and k_cache must be [rows, heads, 192], got {tuple(q.shape)} and {tuple(k_cache.shape)}")
+    Tq, hq, dqk = q.shape
+    rows, hkv, _ = k_cache.shape
+    total, B1 = kv_indices.numel(), cu_q.numel()
+    _check_tensors(("q", q, bf16, q.shape), ("k_cache", k_cache, bf16, (rows, hkv, dqk)),
+                   ("kv_indices", kv_indices, i32, (total,)), ("cu_q", cu_q, i32, (B1,)),
+                   ("kv_indptr", kv_indptr, i32, (B1,)), ("lse", lse, f32, (hq, Tq)), ("prev", prev, f32, (total,)),
+                   ("out", out, f32, (total,)))
+    dims = make_decode_dims(B1 - 1, Tq, total, rows, max_q_len, max_kv_len, hq, hkv, dqk, 128)
+    nbytes = LIB.mimo_decode_key_weights_workspace_size(ctypes.byref(dims))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((total,), dtype=torch.float32, device=q.device)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+    st = LIB.mimo_decode_key_weights(q.data_ptr(), k_cache.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(),
+                                     cu_q.data_ptr(), lse.data_ptr(), None if prev is None else prev.data_ptr(),
+                                     ctypes.byref(dims), int(layer_kind), int(window), float(rope_base),
+                                     int(rope_dims), out.data_ptr(), ws.data_ptr(), nbytes, _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_decode_key_weights")
+    return out
+
+
+def kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first=0, keep_recent=0, stream=None):
+    """Eviction by accumulated attention weight: of each sequence longer than budget, the first keep_first, the
+    last keep_recent and the heaviest of the rest stay.  fp32 weights and int32 kv_indices [total_kv], int32
+    kv_indptr [B + 1] (CUDA).  Returns (new_indices, new_weights, new_indptr, freed): buffers of total_kv entries
+    of which the first new_indptr[B] (freed: the first kv_indptr[B] - new_indptr[B]) are written."""
+    import torch
+    i32, f32 = (torch.int32,), (torch.float32,)
+    total, B1 = kv_indices.numel(), kv_indptr.numel()
+    _check_tensors(("weights", weights, f32, (total,)), ("kv_indices", kv_indices, i32, (total,)),
+                   ("kv_indptr", kv_indptr, i32, (B1,)))
+    with _on(stream):
+        idx, freed = torch.empty_like(kv_indices), torch.empty_like(kv_indices)
+        w, ptr = torch.empty_like(weights), torch.empty_like(kv_indptr)
+    st = LIB.mimo_kv_evict(weights.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(), B1 - 1, total,
+                           int(max_kv_len), int(budget), int(keep_first), int(keep_recent), idx.data_ptr(),
+                           w.data_ptr(), ptr.data_ptr(), freed.data_ptr(), _stream_handle(stream))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_kv_evict")
+    return idx, w, ptr, freed

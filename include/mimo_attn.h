@@ -394,6 +394,132 @@ MIMO_API int mimo_linear_proj(const void* x, const void* w, int64_t tokens, int6
 MIMO_API int mimo_moe_route(const float* logits, const float* bias, int64_t tokens, int num_experts, int top_k,
                             int normalize, int32_t* ids, float* weights, void* stream);
 
+/*
+ * RMS norm in front of the attention and of the experts, with the residual's
+ * addition and an FP8 output:
+ *   h = bf16(x + residual)  (h = x when residual is NULL)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * The norm is of h as it is stored.  All device:
+ *   x, residual  bf16 [tokens, features]; residual may be NULL
+ *   weight       [features], bf16, or fp32 when weight_fp32 != 0
+ *   h            bf16 [tokens, features] or NULL (not written); may be x or residual
+ *   y            bf16 [tokens, features] or NULL
+ *   codes        E4M3 bytes [tokens, features] or NULL: y / scale rounded to
+ *                nearest even, from the FP32 y; scale_inv fp32 [tokens,
+ *                ceil(features / 128)]: max(max |y| / 448, 2^-126) of each 1 x 128
+ *                block, so that mimo_fp8_dequant_blockwise with blocks of 1 x 128
+ *                gives y back.  codes needs scale_inv, and one of y and codes is
+ *                needed.
+ * Sums are FP32.  features: a multiple of 8 (16 with codes) up to 16384, else
+ * MIMO_ERR_UNSUPPORTED; 1e-18 <= eps <= 1e18.  But for h, outputs may not
+ * overlap inputs.  A NaN in a row makes its y NaN.  Does not synchronise.
+ * (The pages name no eps and no norm code; this is the usual RMS norm.)
+ */
+MIMO_API int mimo_rms_norm(const void* x, const void* residual, const void* weight, int weight_fp32, int64_t tokens,
+                           int64_t features, float eps, void* h, void* y, void* codes, float* scale_inv,
+                           void* stream);
+
+/*
+ * Gradient of mimo_rms_norm: with h the stored sum (its h output, or x without a
+ * residual), dy = dL/dy and dh = the gradient that reaches h by its other uses
+ * (NULL = 0), both bf16 [tokens, features],
+ *   dx      bf16 [tokens, features]: dL/dh, which is dL/dx and dL/dresidual
+ *           (the rounding of h taken as the identity); may be dy or dh
+ *   dweight fp32 [features], overwritten
+ * Sums are FP32 in a fixed order: the result does not change from run to run.
+ * workspace: device, 16-byte aligned, at least
+ * mimo_rms_norm_bwd_workspace_size(tokens, features) bytes; calls that overlap
+ * need one each.  Limits as mimo_rms_norm.  Does not synchronise.
+ */
+MIMO_API size_t mimo_rms_norm_bwd_workspace_size(int64_t tokens, int64_t features);
+MIMO_API int mimo_rms_norm_bwd(const void* h, const void* weight, int weight_fp32, const void* dy, const void* dh,
+                               int64_t tokens, int64_t features, float eps, void* dx, float* dweight,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * MoE routing with sigmoid or softmax scores and a group-limited choice:
+ *   score_e = sigmoid(logit_e) or softmax(logits)_e, key_e = fp32(score_e) + bias_e
+ *   a group's score is the sum (FP32) of its two largest keys (its key, if it has
+ *   one expert); the top_groups largest of the num_groups groups of num_experts /
+ *   num_groups consecutive experts are kept, ties to the lower group
+ *   ids: the top_k largest keys of the kept groups, descending, ties to the lower
+ *   expert; weights: scale * score, divided by the chosen scores' sum when
+ *   normalize != 0 (all of them zero: weights zero)
+ * logits fp32 [T, E], bias fp32 [E] or NULL (zero), ids int32 [T, top_k], weights
+ * fp32 [T, top_k], all device.  Scores are FP64 and keys FP32, as in
+ * mimo_moe_route.  A NaN key counts as -inf, so ids are always experts; a NaN
+ * logit makes that score (softmax: every score of the token) NaN.
+ * E up to 512, top_k up to 32, num_groups up to 32 (else MIMO_ERR_UNSUPPORTED);
+ * num_groups divides E, 1 <= top_groups <= num_groups, top_k <= top_groups * E /
+ * num_groups, scale finite (else MIMO_ERR_INVALID_ARG).  logits and bias 16-byte
+ * aligned.  Does not synchronise.
+ */
+typedef enum { MIMO_ROUTE_SIGMOID = 0, MIMO_ROUTE_SOFTMAX = 1 } mimo_route_score;
+MIMO_API int mimo_moe_route_grouped(const float* logits, const float* bias, int64_t tokens, int num_experts,
+                                    int top_k, int num_groups, int top_groups, int score, int normalize, float scale,
+                                    int32_t* ids, float* weights, void* stream);
+
+/*
+ * Gradient of the weights of mimo_moe_route_grouped (and, with sigmoid scores and
+ * scale 1, of mimo_moe_route) with respect to the logits, at the choice `ids`
+ * (the choice itself and the bias have none): dlogits fp32 [T, E], every element
+ * written.  dweights fp32 [T, top_k].  An id outside [0, E) is an empty place and
+ * takes no part; the same id twice adds up.  Limits and alignment as above, and
+ * dlogits 16-byte aligned.  Does not synchronise.
+ */
+MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const float* dweights, int64_t tokens,
+                                int num_experts, int top_k, int score, int normalize, float scale, float* dlogits,
+                                void* stream);
+
+/*
+ * The attention weight each cached key receives from the new queries of a
+ * KV-cache step, summed over the query heads and the sequence's new queries:
+ *   out[e] = (prev ? prev[e] : 0) + sum exp(q~ . k~ / sqrt(192) - lse)
+ * for index-list entry e, over the queries that mimo_attn_decode lets see its
+ * key; lse is that call's.  Arguments as mimo_attn_decode (no V, sink in lse);
+ * prev fp32 [total_kv] or NULL, out fp32 [total_kv], which may be prev.  Entries
+ * whose key no query sees get prev; sequences without new queries are allowed.
+ * The scores are formed with the rotated dims to 22 bits (two FP16 parts), and
+ * the sums are FP32 in a fixed order: the result does not change from run to run.
+ * Range of rotated values as the forward's (MIMO_ERR_RANGE).  Inconsistent
+ * sequences are recorded as MIMO_ERR_BAD_SEQLENS and left unwritten, as are
+ * entries behind the last sequence; cache rows outside [0, cache_rows) count as
+ * zeros and are recorded.
+ * workspace: device, 256-byte aligned, at least
+ * mimo_decode_key_weights_workspace_size(dims) bytes (0 for invalid dims; about
+ * 516 bytes per new token and query head, and 4 per key and KV head); calls that
+ * overlap need one each.  Does not synchronise.
+ */
+MIMO_API size_t mimo_decode_key_weights_workspace_size(const mimo_decode_dims* dims);
+MIMO_API int mimo_decode_key_weights(const void* q, const void* k_cache, const int32_t* kv_indices,
+                                     const int32_t* kv_indptr, const int32_t* cu_q, const float* lse,
+                                     const float* prev, const mimo_decode_dims* dims, int layer_kind, int window,
+                                     double rope_base, int rope_dims, float* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction from the page-size-1 KV cache by accumulated attention weight.  Of
+ * each sequence with more than `budget` entries in the index list, its first
+ * keep_first, its last keep_recent and the entries with the largest weights
+ * between them stay, `budget` in all (ties to the earlier entry; NaN below
+ * everything); the others keep all their entries.  What stays keeps its order.
+ *   weights     fp32 [total_kv], kv_indices int32 [total_kv], kv_indptr int32
+ *               [num_seqs + 1] with kv_indptr[0] = 0 and lengths <= max_kv_len
+ *   new_indices int32, new_weights fp32 [total_kv]: the entries that stay, packed;
+ *               sequence b's start at new_indptr[b] (int32 [num_seqs + 1])
+ *   freed       int32 [total_kv]: the cache rows that left, packed; sequence b's
+ *               start at kv_indptr[b] - new_indptr[b]
+ * Outputs are written up to the new totals only, and may not overlap inputs.
+ * 0 <= keep_first, 0 <= keep_recent, keep_first + keep_recent <= budget.  An
+ * inconsistent kv_indptr is recorded as MIMO_ERR_BAD_SEQLENS and nothing is
+ * written.  The positions of the keys that stay move up with them (a key's
+ * position is its place in the list).  Does not synchronise.
+ */
+MIMO_API int mimo_kv_evict(const float* weights, const int32_t* kv_indices, const int32_t* kv_indptr, int num_seqs,
+                           int total_kv, int max_kv_len, int budget, int keep_first, int keep_recent,
+                           int32_t* new_indices, float* new_weights, int32_t* new_indptr, int32_t* freed,
+                           void* stream);
+
 /* ABI version: (major << 16) | minor. */
 MIMO_API int mimo_attn_version(void);
 
