@@ -4,6 +4,14 @@
 // keep_first, its last keep_recent and, of the rest, those with the largest weights (ties to the earlier
 // entry, NaN below everything) stay, budget in all, in their order.  The kept rows and weights are packed
 // without gaps, and the rows that left are packed in a list of their own.
+//
+// A cluster of C CTAs takes one sequence, each warp a contiguous piece of it.  Weights become unsigned
+// integers of the same order (entries that must stay: the largest), are kept in shared memory, and the
+// budget-th largest is found by a radix select of 11 + 11 + 10 bits: each CTA counts its digits in shared
+// memory, and every CTA adds the cluster's counts over distributed shared memory.  With S(i) and E(i) the
+// entries before i that are above / equal to that threshold and m the equal ones that stay, entry i's place
+// is S(i) + min(E(i), m), so one count per warp and one exchange of the warps' counts place every entry.
+// All of it is integer arithmetic: the result is the same for any C.
 #pragma once
 
 #include <stdint.h>
@@ -15,6 +23,10 @@ namespace mimo {
 namespace ev {
 
 constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kAhead = 8;  // loads of 32 entries that a warp has in flight
+constexpr uint32_t kMust = 0xFFFFFFFFu;  // above every weight's bits
 
 struct EvictParams {
   const float* weights;       // [total_kv]
@@ -26,7 +38,17 @@ struct EvictParams {
   int32_t* freed;             // rows that left
   int32_t num_seqs, total_kv, max_kv_len;
   int32_t budget, first, recent;
+  int32_t key_cap;            // weights' bits that fit in a CTA's shared memory
 };
+
+struct Shared {
+  uint32_t hist[3 * kBins];  // of the three digits
+  uint32_t scan[2][kWarps];   // block-wide sums
+  uint32_t above[kWarps], equal[kWarps];  // the warps' counts
+  uint32_t pick[2];           // digit, entries of it that stay
+};
+// then key_cap words: the bits of the CTA's entries
+constexpr uint32_t kFixedBytes = (sizeof(Shared) + 15) / 16 * 16;
 
 // Bits that order like the weight as unsigned integers: 0 for NaN, then from -inf up; +0 and -0 the same.
 __device__ __forceinline__ uint32_t order_bits(float w) {
@@ -35,124 +57,211 @@ __device__ __forceinline__ uint32_t order_bits(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Inclusive sums of two counts over the CTA's threads (packed in one 64-bit word), and the totals.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* s_warp,
-                                                         unsigned long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += y;
   }
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  unsigned long long before = 0, all = 0;
-  for (int k = 0; k < kThreads / 32; ++k) {
-    if (k < warp) before += s_warp[k];
-    all += s_warp[k];
-  }
-  __syncthreads();
-  total = all;
-  return v + before;
+  return v;
 }
 
-// One CTA per sequence.
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const __grid_constant__ EvictParams P) {
-  __shared__ uint32_t s_hist[256];
-  __shared__ unsigned long long s_warp[kThreads / 32];
-  __shared__ uint32_t s_pick[2];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  // where the sequence's entries go: the kept lengths of the sequences before it
-  long long before = 0;
-  bool ok = true;
-  {
-    unsigned long long mine = 0, all = 0;
-    for (int i = tid; i < P.num_seqs; i += kThreads) {
-      const int lo = __ldg(P.kv_indptr + i), hi = __ldg(P.kv_indptr + i + 1);
-      if (lo < 0 || hi < lo || hi > P.total_kv || hi - lo > P.max_kv_len || (i == 0 && lo != 0)) ok = false;
-      if (i < b && hi > lo) mine += static_cast<unsigned long long>(min(hi - lo, P.budget));
-    }
-    block_scan(mine, s_warp, all);
-    before = static_cast<long long>(all);
+// Inclusive sum over the CTA's threads; `buf` alternates between calls.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* buf, int lane, int warp) {
+  v = warp_scan(v, lane);
+  if (lane == 31) buf[warp] = v;
+  __syncthreads();
+  const uint32_t w = warp_scan(buf[lane], lane);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return warp > 0 ? v + before : v;
+}
+
+// Adds one to hist[d] for the lanes of `live`; one atomic when the live lanes share a digit.
+__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t d, bool live, int lane) {
+  const unsigned m = __ballot_sync(0xffffffffu, live);
+  if (m == 0) return;
+  const int lead = __ffs(m) - 1;
+  const uint32_t d0 = __shfl_sync(0xffffffffu, d, lead);
+  if (__all_sync(0xffffffffu, !live || d == d0)) {
+    if (lane == lead) atomicAdd(&hist[d0], static_cast<uint32_t>(__popc(m)));
+  } else if (live) {
+    atomicAdd(&hist[d], 1u);
   }
-  if (__syncthreads_or(!ok)) {  // an inconsistent index list: report and write nothing
-    if (tid == 0 && b == 0) atomicOr(&g_mimo_error, kErrSeqlens);
+}
+
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
+    kv_evict_kernel(const __grid_constant__ EvictParams P) {
+  extern __shared__ __align__(16) float sm[];
+  Shared* S = reinterpret_cast<Shared*>(sm);
+  const int b = blockIdx.x / C, r = C > 1 ? blockIdx.x % C : 0, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 3 * kBins; i += kThreads) S->hist[i] = 0;
+  // the index list's bounds, and where this sequence's entries go: the kept lengths before it
+  uint32_t mine = 0;
+  bool ok = true;
+  for (int i = tid; i < P.num_seqs; i += kThreads) {
+    const int lo = __ldg(P.kv_indptr + i), hi = __ldg(P.kv_indptr + i + 1);
+    if (lo < 0 || hi < lo || hi > P.total_kv || hi - lo > P.max_kv_len || (i == 0 && lo != 0)) ok = false;
+    if (i < b && hi > lo) mine += static_cast<uint32_t>(min(hi - lo, P.budget));
+  }
+  const uint32_t sum = block_scan(mine, S->scan[0], lane, warp);
+  if (tid == kThreads - 1) S->pick[0] = sum;
+  if (__syncthreads_or(!ok)) {  // inconsistent (every CTA sees the same list): report and write nothing
+    if (tid == 0 && blockIdx.x == 0) atomicOr(&g_mimo_error, kErrSeqlens);
     return;
   }
+  const int before = static_cast<int>(S->pick[0]);
   const int beg = __ldg(P.kv_indptr + b), n = __ldg(P.kv_indptr + b + 1) - beg;
-  const int kept = min(n, P.budget);
-  if (tid == 0) {
+  if (tid == 0 && r == 0) {
     if (b == 0) P.new_indptr[0] = 0;
-    P.new_indptr[b + 1] = static_cast<int32_t>(before + kept);
+    P.new_indptr[b + 1] = before + min(n, P.budget);
   }
   const float* w = P.weights + beg;
   const int32_t* idx = P.kv_indices + beg;
   int32_t* to_idx = P.new_indices + before;
   float* to_w = P.new_weights + before;
   int32_t* away = P.freed + (beg - before);
-  if (n <= P.budget) {
-    for (int i = tid; i < n; i += kThreads) {
+  if (n <= P.budget) {  // the same for every CTA of the cluster
+    for (int i = r * kThreads + tid; i < n; i += C * kThreads) {
       to_idx[i] = __ldg(idx + i);
       to_w[i] = __ldg(w + i);
     }
     return;
   }
-  // the (budget - first - recent)-th largest weight of entries first .. n - recent - 1, digit by digit
-  const int lo = P.first, hi = n - P.recent;
-  uint32_t need = static_cast<uint32_t>(P.budget - P.first - P.recent), prefix = 0;
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) s_hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = lo + tid; i < hi; i += kThreads) {
-      const uint32_t o = order_bits(__ldg(w + i));
-      if ((o & mask) == prefix) atomicAdd(&s_hist[(o >> shift) & 255u], 1u);
+  // this warp's piece [i0, i1), a multiple of 32 entries; its bits are at keys[i - base]
+  const int piece = static_cast<int>(((static_cast<int64_t>(n) + C * kWarps - 1) / (C * kWarps) + 31) / 32 * 32);
+  const int64_t start = static_cast<int64_t>(r * kWarps + warp) * piece;
+  const int i0 = static_cast<int>(min(start, static_cast<int64_t>(n)));
+  const int i1 = static_cast<int>(min(start + piece, static_cast<int64_t>(n)));
+  const bool stored = static_cast<int64_t>(piece) * kWarps <= P.key_cap;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sm) + kFixedBytes / 4 + warp * piece;
+  const int must_from = n - P.recent;
+  auto bits_at = [&](int i) -> uint32_t {
+    const uint32_t o = order_bits(__ldg(w + i));
+    return (i < P.first || i >= must_from) ? kMust : o;
+  };
+  auto key_at = [&](int i) -> uint32_t { return stored ? keys[i - i0] : bits_at(i); };
+  // first digit, while the bits are stored
+  for (int i = i0; i < i1; i += 32 * kAhead) {
+    uint32_t o[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) o[k] = i + 32 * k + lane < i1 ? bits_at(i + 32 * k + lane) : 0u;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const bool live = i + 32 * k + lane < i1;
+      if (live && stored) keys[i + 32 * k + lane - i0] = o[k];
+      count_digit(S->hist, o[k] >> 21, live, lane);
     }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t left = need;
-      int d = 255;
-      for (; d > 0 && s_hist[d] < left; --d) left -= s_hist[d];
-      s_pick[0] = static_cast<uint32_t>(d);
-      s_pick[1] = left;
-    }
-    __syncthreads();
-    prefix |= s_pick[0] << shift;
-    need = s_pick[1];
-    __syncthreads();
   }
-  // of the entries equal to the threshold, the first `need` stay
-  const bool any = P.budget > P.first + P.recent;
-  uint32_t ties = 0, out = 0;
-  for (int base = 0; base < n; base += kThreads) {
-    const int i = base + tid;
-    float v = 0.f;
-    bool keep = false, tie = false;
-    if (i < n) {
-      v = __ldg(w + i);
-      keep = i < lo || i >= hi;
-      if (!keep && any) {
-        const uint32_t o = order_bits(v);
-        keep = o > prefix;
-        tie = o == prefix;
+  uint32_t need = static_cast<uint32_t>(P.budget), prefix = 0;
+  // pass p: digit of `width` bits at `shift`, over the entries that agree with the prefix above it
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const int shift = p == 0 ? 21 : p == 1 ? 10 : 0;
+    if (p > 0) {
+      const int above = p == 1 ? 21 : 10;
+      const uint32_t digit_mask = p == 1 ? 2047u : 1023u;
+      for (int i = i0; i < i1; i += 32) {
+        const bool in = i + lane < i1;
+        const uint32_t o = in ? key_at(i + lane) : 0u;
+        count_digit(S->hist + p * kBins, (o >> shift) & digit_mask, in && (o >> above) == (prefix >> above), lane);
       }
     }
-    unsigned long long total;
-    const unsigned long long t = block_scan(tie ? 1u : 0u, s_warp, total);
-    if (tie && ties + static_cast<uint32_t>(t) <= need) keep = true;
-    ties += static_cast<uint32_t>(total);
-    const unsigned long long k = block_scan(keep ? 1u : 0u, s_warp, total);
-    if (i < n) {
-      const uint32_t at = out + static_cast<uint32_t>(k);  // kept entries up to and with this one
-      if (keep) {
-        to_idx[at - 1] = __ldg(idx + i);
-        to_w[at - 1] = v;
-      } else {
-        away[i - at] = __ldg(idx + i);
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    // the largest digits first: thread t adds bins 2047 - 2t and 2046 - 2t over the cluster
+    const int hi = kBins - 1 - 2 * tid;
+    uint32_t a = 0, c = 0;
+    if (C > 1) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        c += ld_cluster_u32(&S->hist[p * kBins + hi], k);
+        a += ld_cluster_u32(&S->hist[p * kBins + hi - 1], k);
       }
+    } else {
+      c = S->hist[p * kBins + hi];
+      a = S->hist[p * kBins + hi - 1];
     }
-    out += static_cast<uint32_t>(total);
+    const uint32_t upto = block_scan(a + c, S->scan[(p + 1) & 1], lane, warp), from = upto - a - c;
+    if (from < need && upto >= need) {  // one thread, for need >= 1
+      const bool first = from + c >= need;
+      S->pick[0] = static_cast<uint32_t>(first ? hi : hi - 1);
+      S->pick[1] = need - (first ? from : from + c);
+    }
+    __syncthreads();
+    if (need > 0) {
+      prefix |= S->pick[0] << shift;
+      need = S->pick[1];
+    } else {
+      prefix = kMust;  // nothing stays (budget 0: no entry must)
+    }
+    // pick is written again only after the next pass's barriers
   }
+  // counts of entries above and equal to the threshold
+  uint32_t above = 0, equal = 0;
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const uint32_t o = in ? key_at(i + lane) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, in && o > prefix));
+    equal += __popc(__ballot_sync(0xffffffffu, in && o == prefix));
+  }
+  if (lane == 0) {
+    S->above[warp] = above;
+    S->equal[warp] = equal;
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  above = equal = 0;  // those of the warps before this one
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    const bool mine_too = k < r || (k == r && lane < warp);
+    if (C > 1) {
+      if (mine_too) {
+        above += ld_cluster_u32(&S->above[lane], k);
+        equal += ld_cluster_u32(&S->equal[lane], k);
+      }
+    } else if (mine_too) {
+      above += S->above[lane];
+      equal += S->equal[lane];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    above += __shfl_xor_sync(0xffffffffu, above, o);
+    equal += __shfl_xor_sync(0xffffffffu, equal, o);
+  }
+  if (C > 1) cluster_arrive();  // this thread reads no other CTA's memory any more
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32 * kAhead) {
+    int32_t row[kAhead];
+    float wt[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int at = i + 32 * k + lane;
+      row[k] = at < i1 ? __ldg(idx + at) : 0;
+      wt[k] = at < i1 ? __ldg(w + at) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int at = i + 32 * k + lane;
+      const bool in = at < i1;
+      const uint32_t o = in ? key_at(at) : 0u;
+      const unsigned ma = __ballot_sync(0xffffffffu, in && o > prefix), me = __ballot_sync(0xffffffffu, in && o == prefix);
+      const uint32_t e = equal + __popc(me & below);  // equal ones before this entry
+      const uint32_t place = above + __popc(ma & below) + min(e, need);
+      if (in) {
+        if (o > prefix || (o == prefix && e < need)) {
+          to_idx[place] = row[k];
+          to_w[place] = wt[k];
+        } else {
+          away[at - place] = row[k];
+        }
+      }
+      above += __popc(ma);
+      equal += __popc(me);
+    }
+  }
+  if (C > 1) cluster_wait();  // the cluster's other CTAs may still read this one's memory
 }
 
 }  // namespace ev

@@ -757,6 +757,61 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
     rms::rms_norm_bwd_kernel<TPR, V, uint16_t><<<grid, rms::kBwdThreads, smem, stream>>>(P);
 }
 
+// ---------------------------------------------------------------- routing
+template <int P>
+void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, size_t smem,
+                       cudaStream_t stream) {
+  if (R.softmax)
+    rg::route_fast_kernel<P, true><<<grid, rg::kThreads, smem, stream>>>(R, F);
+  else
+    rg::route_fast_kernel<P, false><<<grid, rg::kThreads, smem, stream>>>(R, F);
+}
+
+void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, cudaStream_t stream) {
+  rg::FastShape F;
+  F.S = R.E / R.groups;
+  F.L = 32;
+  while (F.L * R.groups > 32) F.L /= 2;
+  F.P = (F.S + F.L - 1) / F.L;
+  F.vec = F.P % 4 == 0 && F.S == F.L * F.P && F.L * R.groups == 32 && (F.P & (F.P - 1)) == 0;
+  if (F.P <= 1) launch_route_fast<1>(R, F, grid, smem, stream);
+  else if (F.P <= 2) launch_route_fast<2>(R, F, grid, smem, stream);
+  else if (F.P <= 4) launch_route_fast<4>(R, F, grid, smem, stream);
+  else if (F.P <= 8) launch_route_fast<8>(R, F, grid, smem, stream);
+  else if (F.P <= 16) launch_route_fast<16>(R, F, grid, smem, stream);
+  else rg::route_grouped_kernel<<<grid, rg::kThreads, smem, stream>>>(R);  // e.g. 17 groups of 30
+}
+
+// ---------------------------------------------------------------- eviction
+constexpr uint32_t kEvictMaxSmem = 200 * 1024;
+
+template <int C>
+int launch_evict_c(ev::EvictParams& P, int dev, cudaStream_t stream) {
+  static std::atomic<int> state[64];  // 0 unknown, 1 ready, -1 failed
+  if (state[dev].load() == 0)
+    state[dev].store(cudaFuncSetAttribute(ev::kv_evict_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kEvictMaxSmem) == cudaSuccess
+                         ? 1
+                         : -1);
+  if (state[dev].load() != 1) return MIMO_ERR_CUDA;
+  // the longest sequence's piece of a CTA, if it fits
+  const int64_t piece = ((int64_t)P.max_kv_len + C * ev::kWarps - 1) / (C * ev::kWarps);
+  const int64_t need = (piece + 31) / 32 * 32 * ev::kWarps;
+  const int64_t room = (kEvictMaxSmem - ev::kFixedBytes) / 4;
+  P.key_cap = (int32_t)(need <= room ? need : 0);
+  const uint32_t smem = ev::kFixedBytes + (uint32_t)P.key_cap * 4;
+  ev::kv_evict_kernel<C><<<(unsigned)P.num_seqs * C, ev::kThreads, smem, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+}
+
+int launch_evict(ev::EvictParams& P, cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MIMO_ERR_CUDA;
+  if (P.max_kv_len <= 2048) return launch_evict_c<1>(P, dev, stream);
+  if (P.max_kv_len <= 16384) return launch_evict_c<2>(P, dev, stream);
+  return launch_evict_c<8>(P, dev, stream);
+}
+
 // ---------------------------------------------------------------- key weights
 constexpr int64_t kSmsForSplits = 148;  // the split of the query tiles, which sizes the workspace, goes by this
 
@@ -1228,7 +1283,7 @@ int mimo_moe_route_grouped(const float* logits, const float* bias, int64_t token
   P.scale = scale;
   const unsigned grid = (unsigned)std::min<long long>((tokens + rg::kWarps - 1) / rg::kWarps, 16LL * info->sms);
   const size_t smem = (size_t)rg::kWarps * num_experts * 4;
-  rg::route_grouped_kernel<<<grid, rg::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
+  launch_route(P, grid, smem, static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 
@@ -1298,6 +1353,7 @@ int mimo_kv_evict(const float* weights, const int32_t* kv_indices, const int32_t
   if (num_seqs < 1 || total_kv < 0 || max_kv_len < 0 || max_kv_len > total_kv || keep_first < 0 || keep_recent < 0 ||
       (int64_t)keep_first + keep_recent > budget)
     return MIMO_ERR_INVALID_ARG;
+  if (num_seqs > (1 << 24)) return MIMO_ERR_UNSUPPORTED;  // the grid
   if (!kv_indptr || !new_indptr) return MIMO_ERR_INVALID_ARG;
   if (total_kv > 0 && (!weights || !kv_indices || !new_indices || !new_weights || !freed)) return MIMO_ERR_INVALID_ARG;
   for (const void* p : {(const void*)weights, (const void*)kv_indices, (const void*)kv_indptr,
@@ -1318,8 +1374,7 @@ int mimo_kv_evict(const float* weights, const int32_t* kv_indices, const int32_t
   P.budget = budget;
   P.first = keep_first;
   P.recent = keep_recent;
-  ev::kv_evict_kernel<<<(unsigned)num_seqs, ev::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
+  return launch_evict(P, static_cast<cudaStream_t>(stream));
 }
 
 int mimo_attn_version(void) { return (1 << 16) | 6; }

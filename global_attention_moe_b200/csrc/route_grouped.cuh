@@ -10,6 +10,19 @@
 //
 // The choice is defined on FP32 keys of FP64 scores, as the ungrouped router's is, so it does not depend
 // on how the scores are computed, and the tests can ask for equal ids.
+//
+// route_fast_kernel takes it on approximate FP32 keys whose error is bounded, one warp per token:
+//   1. a lane holds P experts of one group in a row (L lanes to a group), forms their approximate keys,
+//      moved up by a constant so that they are positive and order like their bits as integers, puts the
+//      expert's place in the lane into the low bits, and sorts them;
+//   2. a group's two largest come from its lanes' first two by exchanges; its rank among the groups by
+//      comparing with each; lanes of the groups that are not kept drop out;
+//   3. top_k times, the warp's largest first key (one integer reduction) is taken from its lane;
+//   4. where every two neighbours of the k + 1 largest differ by more than twice the error bound, their
+//      order is that of the exact keys: the chosen experts' scores are formed in FP32 and written.
+// Otherwise the experts within the bound of the k-th key (at most 32) take their exact keys in FP64 and are
+// ranked; and where that does not decide either (group scores within the bound, more than 32 candidates,
+// keys that are NaN, infinite or far below the others), route_exact states the definition.
 #pragma once
 
 #include <stdint.h>
@@ -161,13 +174,259 @@ __device__ __forceinline__ void route_exact(const RouteParams& P, int64_t tok, i
   }
 }
 
-// One warp per token.
+// The definition alone, one warp per token: shapes that the fast kernel's lanes do not hold.
 __global__ void __launch_bounds__(kThreads) route_grouped_kernel(const __grid_constant__ RouteParams P) {
   extern __shared__ __align__(16) float sm[];  // E keys per warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + warp; tok < P.T; tok += step)
     route_exact(P, tok, lane, sm + warp * P.E);
+}
+
+// ---------------------------------------------------------------- the fast kernel
+// What the lanes hold: S = E / groups experts to a group, L lanes to a group, P experts to a lane.
+struct FastShape {
+  int S, L, P, vec;  // vec: every lane holds exactly P experts, a multiple of 4
+};
+
+// Descending compare-exchange network (Batcher's odd-even merge sort), N a power of two.
+template <int N>
+__device__ __forceinline__ void sort_desc(int (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
+}
+
+__device__ __forceinline__ float as_float(int k) { return __uint_as_float(static_cast<uint32_t>(k)); }
+
+constexpr int kNone = static_cast<int>(0x80000000u);  // below every key (as a float -0)
+constexpr int kInf = 0x7F800000;
+
+// The exact keys of the experts within `margin` of the k-th approximate one, ranked.  key: the lane's sorted
+// keys.  Returns false when there are more than 32 of them.
+template <int P>
+__device__ __noinline__ bool route_candidates(const RouteParams& R, const FastShape& F, int64_t tok, int lane,
+                                              const int* sorted, int mask, float margin) {
+  const float* x = R.logits + tok * R.E;
+  int at = 0, n = 0, mine = 0;  // the lane's next key; candidates; this lane's candidate
+  float cut = -INFINITY;
+#pragma unroll 1
+  while (true) {
+    const int a = at < P ? sorted[at] : kNone;
+    const int M = __reduce_max_sync(0xffffffffu, a);
+    if (M < 0 || as_float(M) < cut) break;
+    if (n == 32) return false;
+    const int first = __ffs(__ballot_sync(0xffffffffu, a == M)) - 1;
+    if (lane == first) ++at;
+    if (lane == n) mine = (first / F.L) * F.S + (first % F.L) * F.P + (P - 1 - (M & mask));
+    if (++n == R.top_k) cut = as_float(M) - margin;
+  }
+  if (n < R.top_k) return false;
+  double sc = 0.0;
+  if (R.softmax) {
+    float mx = -INFINITY;
+    for (int e = lane; e < R.E; e += 32) mx = fmaxf(mx, __ldg(x + e));
+    const double m = static_cast<double>(warp_max(mx));
+    double S = 0.0;
+    for (int e = lane; e < R.E; e += 32) S += exp(static_cast<double>(__ldg(x + e)) - m);
+    S = warp_sum_f64(S);
+    sc = exp(static_cast<double>(__ldg(x + mine)) - m) / S;
+  } else {
+    sc = nb::route_sigmoid_f64(static_cast<double>(__ldg(x + mine)));
+  }
+  const float key = static_cast<float>(sc) + (R.bias != nullptr ? __ldg(R.bias + mine) : 0.f);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const float o = __shfl_sync(0xffffffffu, key, j);
+    const int e = __shfl_sync(0xffffffffu, mine, j);
+    rank += (o > key || (o == key && e < mine)) ? 1 : 0;
+  }
+  const bool chosen = lane < n && rank < R.top_k;
+  const double total = warp_sum_f64(chosen ? sc : 0.0);
+  if (chosen) {
+    const double w = R.normalize ? (total == 0.0 ? 0.0 : sc / total) : sc;
+    R.ids[tok * R.top_k + rank] = mine;
+    R.weights[tok * R.top_k + rank] = static_cast<float>(w * static_cast<double>(R.scale));
+  }
+  return true;
+}
+
+__device__ __noinline__ void route_exact_call(const RouteParams& R, int64_t tok, int lane, float* s_key) {
+  route_exact(R, tok, lane, s_key);
+}
+
+template <int P, bool kSoftmax>
+__global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_constant__ RouteParams R,
+                                                              const __grid_constant__ FastShape F) {
+  extern __shared__ __align__(16) float sm[];  // E keys per warp (route_exact)
+  constexpr int kMask = P - 1;                 // low bits of a key: P - 1 - place in the lane
+  constexpr int kDepth = P < 4 ? P : 4;        // keys of a lane that the fast path can take
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane / F.L, in_group = (lane % F.L) * F.P;
+  const int count = g < R.groups ? max(0, min(F.P, F.S - in_group)) : 0;
+  const int e0 = count > 0 ? g * F.S + in_group : 0;
+  // biases moved up by the least of them (those far below all others aside), so that keys are positive
+  float bl[P], low = 0.f;
+#pragma unroll
+  for (int m = 0; m < P; ++m) bl[m] = 0.f;
+  if (R.bias != nullptr) {
+    low = INFINITY;
+#pragma unroll
+    for (int m = 0; m < P; ++m)
+      if (m < count) {
+        bl[m] = __ldg(R.bias + e0 + m);
+        if (bl[m] > -1024.f) low = fminf(low, bl[m]);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    if (!(fabsf(low) < 1e30f)) low = 0.f;
+#pragma unroll
+    for (int m = 0; m < P; ++m) bl[m] -= low;
+  }
+  const float off = fabsf(low);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  float xn[P];  // the next token's logits
+  auto load = [&](int64_t t) {
+    if (P >= 4 && F.vec) {
+      const float4* p = reinterpret_cast<const float4*>(R.logits + t * R.E + e0);
+#pragma unroll
+      for (int m = 0; m < P / 4; ++m) {
+        const float4 v = t < R.T ? __ldg(p + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+        xn[4 * m] = v.x, xn[4 * m + 1] = v.y, xn[4 * m + 2] = v.z, xn[4 * m + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < P; ++m) xn[m] = t < R.T && m < count ? __ldg(R.logits + t * R.E + e0 + m) : -INFINITY;
+    }
+  };
+  load(tok);
+#pragma unroll 1
+  for (; tok < R.T; tok += step) {
+    float sc[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) sc[m] = xn[m];
+    load(tok + step);  // in flight meanwhile
+    float mx = 0.f, inv = 1.f;
+    if (kSoftmax) {
+      mx = sc[0];
+#pragma unroll
+      for (int m = 1; m < P; ++m) mx = fmaxf(mx, sc[m]);
+      mx = warp_max(mx);
+      float sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        sc[m] = __expf(sc[m] - mx);
+        sum += sc[m];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      inv = __fdividef(1.f, sum);
+#pragma unroll
+      for (int m = 0; m < P; ++m) sc[m] *= inv;
+    } else {
+#pragma unroll
+      for (int m = 0; m < P; ++m) sc[m] = nb::route_sigmoid_approx(sc[m]);
+    }
+    int key[P];
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      const int k = static_cast<int>(__float_as_uint(sc[m] + bl[m]));
+      key[m] = m < count ? (k & ~kMask) | (P - 1 - m) : kNone;
+    }
+    sort_desc<P>(key);
+    // A bound on twice the error of a key: the approximate sigmoid's 2^-21 (neighbors.cuh); for softmax, with
+    // d = max - x, exp's (2 + 1.173 d) 2^-23, the sum's the same averaged over the scores (d below ln 512
+    // there) and the division's, under 2^-18 of the score; the place in the low bits, at most 15 2^-23 of the
+    // key; FP32 roundings of the score, the bias's move and the sums.
+    const int top = __reduce_max_sync(0xffffffffu, key[0]);
+    const float margin = (kSoftmax ? 0.f : 0x1p-19f) + 0x1p-16f * (as_float(top) + off);
+    bool slow = top >= kInf;
+    if (R.top_groups < R.groups) {
+      float a = as_float(key[0]), b = P > 1 ? as_float(key[P > 1 ? 1 : 0]) : -0.f;
+      for (int o = 1; o < F.L; o <<= 1) {
+        const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+        a = fmaxf(a, a2);
+      }
+      const float gs = F.S > 1 ? a + b : a;
+      int rank = 0;
+      for (int j = 0; j < R.groups; ++j) {  // exactly top_groups are kept
+        const float o = __shfl_sync(0xffffffffu, gs, j * F.L);
+        rank += (o > gs || (o == gs && j < g)) ? 1 : 0;
+      }
+      const bool kept = rank < R.top_groups;
+      const int bits = static_cast<int>(__float_as_uint(gs));
+      const int least = __reduce_min_sync(0xffffffffu, g < R.groups && kept ? bits : 0x7FFFFFFF);
+      const int most = max(0, __reduce_max_sync(0xffffffffu, g < R.groups && !kept ? bits : 0));
+      slow = slow || least < 0 || !(as_float(least) - as_float(most) > 2.f * margin);
+      if (!kept) {
+#pragma unroll
+        for (int m = 0; m < P; ++m) key[m] = kNone;
+      }
+    }
+    if (!slow) {
+      int h[kDepth];
+#pragma unroll
+      for (int m = 0; m < kDepth; ++m) h[m] = key[m];
+      int M = 0;
+      unsigned from = 0;  // lane c: the c-th largest key and the lane it came from
+#pragma unroll 1
+      for (int c = 0; c < R.top_k; ++c) {
+        const int best = __reduce_max_sync(0xffffffffu, h[0]);
+        const bool here = h[0] == best;
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (lane == c) {
+          M = best;
+          from = who;
+        }
+#pragma unroll
+        for (int m = 0; m + 1 < kDepth; ++m) h[m] = here ? h[m + 1] : h[m];
+        h[kDepth - 1] = here ? kNone : h[kDepth - 1];
+      }
+      const int next = __reduce_max_sync(0xffffffffu, h[0]);
+      const int after = __shfl_sync(0xffffffffu, M, lane + 1 < 32 ? lane + 1 : 31);
+      const float gap = as_float(M) - as_float(lane == R.top_k - 1 ? next : after);
+      const float kth = as_float(__shfl_sync(0xffffffffu, M, R.top_k - 1));
+      bool unsure = P > kDepth && as_float(key[P > kDepth ? kDepth : 0]) > kth - margin;
+      int id = 0;
+      float x = 0.f;
+      if (lane < R.top_k) {
+        unsure = unsure || M < 0 || !(gap > margin) || __popc(from) != 1;
+        const int src = __ffs(from) - 1;
+        id = (src / F.L) * F.S + (src % F.L) * F.P + (P - 1 - (M & kMask));
+        if (!unsure) x = __ldg(R.logits + tok * R.E + id);
+        unsure = unsure || x - mx < -80.f;  // scores that FP32 may not hold
+      }
+      if (!__any_sync(0xffffffffu, unsure)) {
+        float s = 0.f;
+        if (lane < R.top_k) s = kSoftmax ? expf(x - mx) * inv : __fdiv_rn(1.f, 1.f + expf(-x));
+        if (R.normalize) {
+          float total = s;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+          s = __fdiv_rn(s, total);
+        }
+        if (lane < R.top_k) {
+          R.ids[tok * R.top_k + lane] = id;
+          R.weights[tok * R.top_k + lane] = s * R.scale;
+        }
+      } else {
+        slow = !route_candidates<P>(R, F, tok, lane, key, kMask, margin);
+      }
+    }
+    if (slow) route_exact_call(R, tok, lane, sm + warp * R.E);
+  }
 }
 
 struct RouteBwdParams {

@@ -10,6 +10,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmimo_attn.so")
 
@@ -149,7 +151,6 @@ def bwd(q, k, v, sink, cu_seqlens, max_seqlen, layer_kind, window, rope_base, ou
     """Gradients of the forward: q/k/v/out/dout bf16 CUDA tensors, lse / dlse fp32 [Hq, T] (dlse may be
     None).  Returns (dq fp32 [T, Hq, 192], dk fp32 [T, Hkv, 192], dv fp32 [T, Hkv, 128], dsink fp32 [Hq] or
     None)."""
-    import torch
     T, hq, dqk = q.shape
     hkv, dv_ = v.shape[1], v.shape[2]
     dq = torch.empty((T, hq, dqk), dtype=torch.float32, device=q.device)
@@ -169,7 +170,6 @@ def bwd(q, k, v, sink, cu_seqlens, max_seqlen, layer_kind, window, rope_base, ou
 
 def fp8_dequant_blockwise(codes, scale_inv, block=(128, 128), out=None, stream=None):
     """uint8 E4M3 codes [rows, cols] and fp32 scale_inv [ceil(rows/b0), ceil(cols/b1)] (CUDA) -> bf16."""
-    import torch
     rows, cols = codes.shape
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
@@ -182,7 +182,6 @@ def fp8_dequant_blockwise(codes, scale_inv, block=(128, 128), out=None, stream=N
 
 def qkv_split(fused, num_q_heads, num_kv_heads, stream=None):
     """bf16 fused [T, Hkv * (Hq/Hkv*192 + 320)] (CUDA) -> q [T, Hq, 192], k [T, Hkv, 192], v [T, Hkv, 128]."""
-    import torch
     T = fused.shape[0]
     q = torch.empty((T, num_q_heads, 192), dtype=torch.bfloat16, device=fused.device)
     k = torch.empty((T, num_kv_heads, 192), dtype=torch.bfloat16, device=fused.device)
@@ -206,7 +205,6 @@ def set_bwd_kernel(choice: int) -> None:
 def linear_proj(x, w, out=None, stream=None):
     """Output projection y = x . w^T: bf16 x [T, K] or the attention output [T, Hq, 128] (CUDA), bf16 w
     [N, K] (a Linear weight) -> bf16 y [T, N] (cuBLAS, FP32 accumulation)."""
-    import torch
     T = x.shape[0]
     feats = 1
     for d in x.shape[1:]:
@@ -225,7 +223,6 @@ def linear_proj(x, w, out=None, stream=None):
 
 def moe_route(logits, bias, top_k=8, normalize=True, stream=None):
     """fp32 logits [T, E] and bias [E] (CUDA) -> ids int32 [T, top_k], weights fp32 [T, top_k]."""
-    import torch
     T, E = logits.shape
     ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
     w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
@@ -261,10 +258,16 @@ def make_dims(num_seqs, total_tokens, max_seqlen, hq, hkv, dqk=192, dv=128) -> D
     return Dims(int(num_seqs), int(total_tokens), int(max_seqlen), int(hq), int(hkv), int(dqk), int(dv))
 
 
+# the current stream of a device as an integer: torch.cuda.current_stream() builds a Python stream object
+# (3.2 us of a 16 us call), this reads the handle (0.1 us); without it the object is built
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream):
-    import torch
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def fwd_raw(q_ptr, k_ptr, v_ptr, sink_ptr, cu_ptr, dims: Dims, layer_kind, window, rope_base, rope_dims, v_scale,
@@ -279,7 +282,6 @@ def fwd(q, k, v, sink, cu_seqlens, max_seqlen, layer_kind, window, rope_base, ro
         out=None, lse=None, stream=None):
     """Attention forward on CUDA tensors (bf16 q/k/v in THD layout, int32 cu_seqlens,
     fp32 sink or None).  Returns (out bf16 [T, Hq, 128], lse fp32 [Hq, T])."""
-    import torch
     T, hq, dqk = q.shape
     hkv, dv = k.shape[1], v.shape[2]
     for t in (q, k, v):
@@ -362,7 +364,6 @@ def decode(q, k_cache, v_cache, kv_indices, kv_indptr, cu_q, sink, max_q_len, ma
     """New query tokens against a page-size-1 KV cache (CUDA tensors: bf16 q [Tq, Hq, 192], bf16 caches
     [rows, Hkv, 192] / [rows, Hkv, 128], int32 kv_indices / kv_indptr / cu_q, fp32 sink or None).
     Returns (out bf16 [Tq, Hq, 128], lse fp32 [Hq, Tq])."""
-    import torch
     Tq, hq, dqk = q.shape
     rows, hkv, dv = v_cache.shape
     for t in (q, k_cache, v_cache):
@@ -382,60 +383,53 @@ def decode(q, k_cache, v_cache, kv_indices, kv_indptr, cu_q, sink, max_q_len, ma
     return out, lse
 
 
-def _check_tensors(*specs):
-    """Each spec: (name, tensor, dtypes, shape); None tensors pass.  Contiguous CUDA tensors of the current
-    device only: kernels are launched there, and rows are read as one dense block."""
-    import torch
-    dev = torch.cuda.current_device()
-    for name, t, dtypes, shape in specs:
-        if t is None:
-            continue
-        if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of {' or '.join(map(str, dtypes))} with shape "
-                             f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                             f"{'' if t.is_contiguous() else ', not contiguous'}")
-        if t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _on(stream):
-    """Outputs and workspaces are allocated on the stream the kernels run on, so that memory another stream
-    still uses is never handed out."""
-    import contextlib
-
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _refuse(name, t, dtype, shape, dev):
+    dt = " or ".join(map(str, dtype)) if isinstance(dtype, tuple) else str(dtype)
+    raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on the current device cuda:{dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _norm(x, weight, residual, eps, with_y, with_fp8, stream):
-    import torch
-    bf16 = (torch.bfloat16,)
+def _check(name, t, dtype, shape, dev):
+    """Contiguous CUDA tensors of the current device only: kernels are launched there, and rows are read as one
+    dense block."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, dev)
+
+
+def _norm_checks(x, name, weight):
     if x.dim() != 2:
-        raise ValueError(f"x must be [tokens, features], got {tuple(x.shape)}")
-    T, H = x.shape
-    _check_tensors(("x", x, bf16, x.shape), ("weight", weight, (torch.bfloat16, torch.float32), (H,)),
-                   ("residual", residual, bf16, x.shape))
-    y = h = codes = scale = None
-    with _on(stream):
-        if residual is not None:
-            h = torch.empty_like(x)
-        if with_y:
-            y = torch.empty_like(x)
-        if with_fp8:
-            codes = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-            scale = torch.empty((T, (H + 127) // 128), dtype=torch.float32, device=x.device)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    st = LIB.mimo_rms_norm(x.data_ptr(), ptr(residual), weight.data_ptr(), int(weight.dtype == torch.float32), T, H,
-                           float(eps), ptr(h), ptr(y), ptr(codes), ptr(scale), _stream_handle(stream))
-    if st != OK:
-        raise MimoAttnError(st, "mimo_rms_norm")
-    return y, codes, scale, x if h is None else h
+        raise ValueError(f"{name} must be [tokens, features], got {tuple(x.shape)}")
+    dev = torch.cuda.current_device()
+    _check(name, x, _BF16, x.shape, dev)
+    w32 = weight.dtype is _F32
+    if not w32 and weight.dtype is not _BF16:
+        _refuse("weight", weight, (_BF16, _F32), x.shape[1:], dev)
+    _check("weight", weight, weight.dtype, x.shape[1:], dev)
+    return dev, w32
 
 
+# With a stream of the caller's, outputs and workspaces are allocated on that stream too (the calls below run
+# again under it): memory that another stream still uses is never handed out.
 def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
     """RMS norm of x (+ residual): bf16 x / residual [T, H] (CUDA), weight [H] bf16 or fp32.  Returns (y bf16
     [T, H], h bf16 [T, H]); h = bf16(x + residual) is the new residual stream (x itself without a residual)."""
-    y, _, _, h = _norm(x, weight, residual, eps, True, False, stream)
+    dev, w32 = _norm_checks(x, "x", weight)
+    if residual is not None:
+        _check("residual", residual, _BF16, x.shape, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm(x, weight, residual, eps)
+    T, H = x.shape
+    y = torch.empty_like(x)
+    h = x if residual is None else torch.empty_like(x)
+    st = LIB.mimo_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), w32, T, H,
+                           eps, None if residual is None else h.data_ptr(), y.data_ptr(), None, None,
+                           _stream_handle(None))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_rms_norm")
     return y, h
 
 
@@ -443,28 +437,43 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, with_bf16=False, stream=Non
     """The same with y as E4M3 bytes and one scale per 1 x 128 block (fp8_dequant_blockwise(codes, scale_inv,
     (1, 128)) gives it back).  Returns (codes uint8 [T, H], scale_inv fp32 [T, ceil(H/128)], h), and y in bf16
     as a fourth with with_bf16."""
-    y, codes, scale, h = _norm(x, weight, residual, eps, bool(with_bf16), True, stream)
+    dev, w32 = _norm_checks(x, "x", weight)
+    if residual is not None:
+        _check("residual", residual, _BF16, x.shape, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_fp8(x, weight, residual, eps, with_bf16)
+    T, H = x.shape
+    codes = torch.empty_like(x, dtype=torch.uint8)
+    scale = x.new_empty((T, (H + 127) // 128), dtype=_F32)
+    h = x if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x) if with_bf16 else None
+    st = LIB.mimo_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), w32, T, H,
+                           eps, None if residual is None else h.data_ptr(), y.data_ptr() if with_bf16 else None,
+                           codes.data_ptr(), scale.data_ptr(), _stream_handle(None))
+    if st != OK:
+        raise MimoAttnError(st, "mimo_rms_norm")
     return (codes, scale, h, y) if with_bf16 else (codes, scale, h)
 
 
 def rms_norm_bwd(h, weight, dy, dh=None, eps=1e-6, stream=None):
     """Gradients of rms_norm: h as it returned it (bf16 [T, H]), dy = dL/dy and dh = dL/dh by h's other uses
     (None: 0), bf16.  Returns (dx bf16 [T, H], the gradient of x and of the residual; dweight fp32 [H])."""
-    import torch
-    bf16 = (torch.bfloat16,)
-    if h.dim() != 2:
-        raise ValueError(f"h must be [tokens, features], got {tuple(h.shape)}")
+    dev, w32 = _norm_checks(h, "h", weight)
+    _check("dy", dy, _BF16, h.shape, dev)
+    if dh is not None:
+        _check("dh", dh, _BF16, h.shape, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_bwd(h, weight, dy, dh, eps)
     T, H = h.shape
-    _check_tensors(("h", h, bf16, h.shape), ("weight", weight, (torch.bfloat16, torch.float32), (H,)),
-                   ("dy", dy, bf16, h.shape), ("dh", dh, bf16, h.shape))
     nbytes = LIB.mimo_rms_norm_bwd_workspace_size(T, H)
-    with _on(stream):
-        dx = torch.empty_like(h)
-        dw = torch.empty((H,), dtype=torch.float32, device=h.device)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=h.device)
-    st = LIB.mimo_rms_norm_bwd(h.data_ptr(), weight.data_ptr(), int(weight.dtype == torch.float32), dy.data_ptr(),
-                               None if dh is None else dh.data_ptr(), T, H, float(eps), dx.data_ptr(), dw.data_ptr(),
-                               ws.data_ptr(), nbytes, _stream_handle(stream))
+    dx = torch.empty_like(h)
+    dw = torch.empty_like(weight, dtype=_F32)
+    ws = h.new_empty((nbytes,), dtype=torch.uint8)
+    st = LIB.mimo_rms_norm_bwd(h.data_ptr(), weight.data_ptr(), w32, dy.data_ptr(),
+                               None if dh is None else dh.data_ptr(), T, H, eps, dx.data_ptr(), dw.data_ptr(),
+                               ws.data_ptr(), nbytes, _stream_handle(None))
     if st != OK:
         raise MimoAttnError(st, "mimo_rms_norm_bwd")
     return dx, dw
@@ -478,18 +487,21 @@ def moe_route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, sc
     """Routing with sigmoid or softmax scores, limited to the top_groups best of num_groups expert groups (a
     group's score: the sum of its two largest score + bias).  fp32 logits [T, E] and bias [E] or None (CUDA) ->
     ids int32 [T, top_k], weights fp32 [T, top_k] (scale times the scores, normalised to sum to one first)."""
-    import torch
-    f32 = (torch.float32,)
     if logits.dim() != 2:
         raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
+    dev = torch.cuda.current_device()
+    _check("logits", logits, _F32, logits.shape, dev)
+    if bias is not None:
+        _check("bias", bias, _F32, logits.shape[1:], dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_grouped(logits, bias, top_k, num_groups, top_groups, score, normalize, scale)
     T, E = logits.shape
-    _check_tensors(("logits", logits, f32, logits.shape), ("bias", bias, f32, (E,)))
-    with _on(stream):
-        ids = torch.empty((T, max(int(top_k), 0)), dtype=torch.int32, device=logits.device)
-        w = torch.empty((T, max(int(top_k), 0)), dtype=torch.float32, device=logits.device)
-    st = LIB.mimo_moe_route_grouped(logits.data_ptr(), None if bias is None else bias.data_ptr(), T, E, int(top_k),
-                                    int(num_groups), int(top_groups), int(score), int(bool(normalize)), float(scale),
-                                    ids.data_ptr(), w.data_ptr(), _stream_handle(stream))
+    w = logits.new_empty((T, top_k if top_k > 0 else 0))
+    ids = torch.empty_like(w, dtype=_I32)
+    st = LIB.mimo_moe_route_grouped(logits.data_ptr(), None if bias is None else bias.data_ptr(), T, E, top_k,
+                                    num_groups, top_groups, score, bool(normalize), scale, ids.data_ptr(),
+                                    w.data_ptr(), _stream_handle(None))
     if st != OK:
         raise MimoAttnError(st, "mimo_moe_route_grouped")
     return ids, w
@@ -499,18 +511,20 @@ def moe_route_bwd(logits, ids, dweights, score=ROUTE_SIGMOID, normalize=True, sc
     """Gradient of moe_route_grouped's weights (or, with the defaults, moe_route's) with respect to the logits:
     fp32 logits [T, E], int32 ids and fp32 dweights [T, top_k] (CUDA) -> dlogits fp32 [T, E].  An id outside
     [0, E) is an empty place."""
-    import torch
-    f32 = (torch.float32,)
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError(f"logits and ids must be [tokens, ...], got {tuple(logits.shape)} and {tuple(ids.shape)}")
+    dev = torch.cuda.current_device()
     T, E = logits.shape
     k = ids.shape[1]
-    _check_tensors(("logits", logits, f32, logits.shape), ("ids", ids, (torch.int32,), (T, k)),
-                   ("dweights", dweights, f32, (T, k)))
-    with _on(stream):
-        d = torch.empty_like(logits)
-    st = LIB.mimo_moe_route_bwd(logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), T, E, k, int(score),
-                                int(bool(normalize)), float(scale), d.data_ptr(), _stream_handle(stream))
+    _check("logits", logits, _F32, logits.shape, dev)
+    _check("ids", ids, _I32, (T, k), dev)
+    _check("dweights", dweights, _F32, (T, k), dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_bwd(logits, ids, dweights, score, normalize, scale)
+    d = torch.empty_like(logits)
+    st = LIB.mimo_moe_route_bwd(logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), T, E, k, score,
+                                bool(normalize), scale, d.data_ptr(), _stream_handle(None))
     if st != OK:
         raise MimoAttnError(st, "mimo_moe_route_bwd")
     return d
@@ -521,27 +535,36 @@ def decode_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, max_q_len, 
     """Attention weight each cached key receives from a decode() step's new queries, summed over the query heads
     and the sequence's queries: arguments as decode (lse fp32 [Hq, Tq] as it returned it), prev fp32 [total_kv]
     or None is added.  Returns fp32 [total_kv], beside kv_indices (out, which may be prev, if given)."""
-    import torch
-    bf16, i32, f32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
-    if q.dim() != 3 or k_cache.dim() != 3:
-        raise ValueError(f"q and k_cache must be [rows, heads, 192], got {tuple(q.shape)} and {tuple(k_cache.shape)}")
+    if q.dim() != 3 or k_cache.dim() != 3 or kv_indices.dim() != 1 or cu_q.dim() != 1:
+        raise ValueError(f"q and k_cache must be [rows, heads, 192] and the index lists flat, got {tuple(q.shape)}, "
+                         f"{tuple(k_cache.shape)}, {tuple(kv_indices.shape)}, {tuple(cu_q.shape)}")
+    dev = torch.cuda.current_device()
     Tq, hq, dqk = q.shape
     rows, hkv, _ = k_cache.shape
-    total, B1 = kv_indices.numel(), cu_q.numel()
-    _check_tensors(("q", q, bf16, q.shape), ("k_cache", k_cache, bf16, (rows, hkv, dqk)),
-                   ("kv_indices", kv_indices, i32, (total,)), ("cu_q", cu_q, i32, (B1,)),
-                   ("kv_indptr", kv_indptr, i32, (B1,)), ("lse", lse, f32, (hq, Tq)), ("prev", prev, f32, (total,)),
-                   ("out", out, f32, (total,)))
-    dims = make_decode_dims(B1 - 1, Tq, total, rows, max_q_len, max_kv_len, hq, hkv, dqk, 128)
-    nbytes = LIB.mimo_decode_key_weights_workspace_size(ctypes.byref(dims))
-    with _on(stream):
-        if out is None:
-            out = torch.empty((total,), dtype=torch.float32, device=q.device)
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+    total, B1 = kv_indices.shape[0], cu_q.shape[0]
+    _check("q", q, _BF16, q.shape, dev)
+    _check("k_cache", k_cache, _BF16, (rows, hkv, dqk), dev)
+    _check("kv_indices", kv_indices, _I32, (total,), dev)
+    _check("kv_indptr", kv_indptr, _I32, (B1,), dev)
+    _check("cu_q", cu_q, _I32, (B1,), dev)
+    _check("lse", lse, _F32, (hq, Tq), dev)
+    for name, t in (("prev", prev), ("out", out)):
+        if t is not None:
+            _check(name, t, _F32, (total,), dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, max_q_len, max_kv_len, layer_kind,
+                                      window, rope_base, rope_dims, prev, out)
+    dims = DecodeDims(B1 - 1, Tq, total, rows, max_q_len, max_kv_len, hq, hkv, dqk, 128)
+    ref = ctypes.byref(dims)
+    nbytes = LIB.mimo_decode_key_weights_workspace_size(ref)
+    if out is None:
+        out = lse.new_empty((total,))
+    ws = lse.new_empty((nbytes,), dtype=torch.uint8)
     st = LIB.mimo_decode_key_weights(q.data_ptr(), k_cache.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(),
-                                     cu_q.data_ptr(), lse.data_ptr(), None if prev is None else prev.data_ptr(),
-                                     ctypes.byref(dims), int(layer_kind), int(window), float(rope_base),
-                                     int(rope_dims), out.data_ptr(), ws.data_ptr(), nbytes, _stream_handle(stream))
+                                     cu_q.data_ptr(), lse.data_ptr(), None if prev is None else prev.data_ptr(), ref,
+                                     layer_kind, window, rope_base, rope_dims, out.data_ptr(), ws.data_ptr(), nbytes,
+                                     _stream_handle(None))
     if st != OK:
         raise MimoAttnError(st, "mimo_decode_key_weights")
     return out
@@ -552,17 +575,21 @@ def kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first=0, k
     last keep_recent and the heaviest of the rest stay.  fp32 weights and int32 kv_indices [total_kv], int32
     kv_indptr [B + 1] (CUDA).  Returns (new_indices, new_weights, new_indptr, freed): buffers of total_kv entries
     of which the first new_indptr[B] (freed: the first kv_indptr[B] - new_indptr[B]) are written."""
-    import torch
-    i32, f32 = (torch.int32,), (torch.float32,)
-    total, B1 = kv_indices.numel(), kv_indptr.numel()
-    _check_tensors(("weights", weights, f32, (total,)), ("kv_indices", kv_indices, i32, (total,)),
-                   ("kv_indptr", kv_indptr, i32, (B1,)))
-    with _on(stream):
-        idx, freed = torch.empty_like(kv_indices), torch.empty_like(kv_indices)
-        w, ptr = torch.empty_like(weights), torch.empty_like(kv_indptr)
-    st = LIB.mimo_kv_evict(weights.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(), B1 - 1, total,
-                           int(max_kv_len), int(budget), int(keep_first), int(keep_recent), idx.data_ptr(),
-                           w.data_ptr(), ptr.data_ptr(), freed.data_ptr(), _stream_handle(stream))
+    if kv_indices.dim() != 1 or kv_indptr.dim() != 1:
+        raise ValueError(f"the index lists must be flat, got {tuple(kv_indices.shape)} and {tuple(kv_indptr.shape)}")
+    dev = torch.cuda.current_device()
+    total, B1 = kv_indices.shape[0], kv_indptr.shape[0]
+    _check("weights", weights, _F32, (total,), dev)
+    _check("kv_indices", kv_indices, _I32, (total,), dev)
+    _check("kv_indptr", kv_indptr, _I32, (B1,), dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first, keep_recent)
+    idx, freed = torch.empty_like(kv_indices), torch.empty_like(kv_indices)
+    w, ptr = torch.empty_like(weights), torch.empty_like(kv_indptr)
+    st = LIB.mimo_kv_evict(weights.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(), B1 - 1, total, max_kv_len,
+                           budget, keep_first, keep_recent, idx.data_ptr(), w.data_ptr(), ptr.data_ptr(),
+                           freed.data_ptr(), _stream_handle(None))
     if st != OK:
         raise MimoAttnError(st, "mimo_kv_evict")
     return idx, w, ptr, freed

@@ -110,6 +110,8 @@ def build(out_dir: str, src_root: str = ROOT, mutations=()) -> str:
             s = s.replace("g_launch_ok = hemu::launch(", "hemu::g_launch_failed |= !hemu::launch(")
             # the SM-pair kernel runs in two-CTA clusters
             s = re.sub(r"(\[&\] \{ attn_fwd_swa2_kernel\([^;]*\); \})\);", r"\1, 2);", s)
+            # the eviction kernel's clusters have as many CTAs as its template argument says
+            s = re.sub(r"(\[&\] \{ ev::kv_evict_kernel<(\w+)>\([^;]*\); \})\);", r"\1, \2);", s)
         with open(p, "w") as f:
             f.write(s)
     tu = os.path.join(out_dir, "library_host.cpp")

@@ -540,4 +540,15 @@ inline bool g_tc_reset_registered = [] {
   return true;
 }();
 
+// ---------------------------------------------------------------- clusters (arrive does not wait: the
+// model's cluster barrier stands where the second half does)
+inline void cluster_arrive() {}
+inline void cluster_wait() { hemu::cluster_barrier(); }
+inline void cluster_sync() { hemu::cluster_barrier(); }
+inline uint32_t ld_cluster_u32(const uint32_t* p, int rank) {
+  uint32_t v;
+  std::memcpy(&v, hemu::g_smem_cta[rank] + (reinterpret_cast<const uint8_t*>(p) - hemu::g_smem), 4);
+  return v;
+}
+
 }  // namespace mimo

@@ -400,6 +400,18 @@ inline unsigned __ballot_sync(unsigned, int pred) {
   hemu::syncwarp();
   return r;
 }
+template <class F>
+inline int hemu_reduce(int v, F f) {
+  const int l = hemu::lin_tid() % 32, w = hemu::warp_slot();
+  hemu::g_xch[w][l] = static_cast<uint32_t>(v);
+  hemu::syncwarp();
+  int r = static_cast<int>(static_cast<uint32_t>(hemu::g_xch[w][0]));
+  for (int i = 1; i < 32; ++i) r = f(r, static_cast<int>(static_cast<uint32_t>(hemu::g_xch[w][i])));
+  hemu::syncwarp();
+  return r;
+}
+inline int __reduce_max_sync(unsigned, int v) { return hemu_reduce(v, [](int a, int b) { return a > b ? a : b; }); }
+inline int __reduce_min_sync(unsigned, int v) { return hemu_reduce(v, [](int a, int b) { return a < b ? a : b; }); }
 inline int __popc(unsigned v) { return __builtin_popcount(v); }
 inline int __ffs(unsigned v) { return __builtin_ffs(static_cast<int>(v)); }
 inline float __fdiv_rn(float a, float b) { return a / b; }

@@ -254,7 +254,8 @@ CASES = {
         (2, 512, 32, 32, 20, False, True, True, 54), (3, 160, 6, 8, 3, True, True, False, 55),
         (2, 1, 1, 1, 1, False, True, False, 56), (2, 7, 3, 7, 3, True, True, True, 57),
         (3, 72, 8, 2, 2, False, True, False, 58), (4, 128, 4, 4, 2, True, True, True, 59),
-        (3, 64, 12, 8, 2, False, True, True, 60), (2, 384, 8, 1, 1, True, False, False, 61))],
+        (3, 64, 12, 8, 2, False, True, True, 60), (2, 384, 8, 1, 1, True, False, False, 61), (3, 510, 8, 17, 5, False, True, True, 62), (4, 96, 8, 3, 2, True, True, True, 63),
+        (4, 224, 8, 7, 3, False, True, True, 64), (3, 256, 32, 8, 1, True, True, False, 65))],
     "route_kinds": lambda be: [check_route(be, 4, E, 8, groups, top, softmax, True, bias, 70, kind)
                                for kind in ("ties", "near", "flat", "far", "masked")
                                for E, groups, top, softmax, bias in ((256, 8, 4, False, True), (256, 1, 1, True, False),
@@ -284,6 +285,9 @@ CASES = {
                              ([40], 0, 0, 0), ([1500, 2300, 30], 1024, 0, 1024), ([200], 10, 10, 0), ([1, 1, 1], 0, 0, 0),
                              ([3000], 1500, 3, 7)))
                          for kind in ("spread", "ties", "flat", "wild")],
+    # eight CTAs per sequence; then more entries than their shared memory holds
+    "evict_long": lambda be: [check_evict(be, *c) for c in (([17000, 5, 300], 3000, 4, 100, 160, "spread"), ([16385], 9000, 0, 1, 161, "ties"),
+                                                            ([400001], 150001, 7, 1000, 162, "wild"))],
 }
 
 
