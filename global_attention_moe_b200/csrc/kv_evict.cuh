@@ -76,19 +76,6 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* buf, int la
   return warp > 0 ? v + before : v;
 }
 
-// Adds one to hist[d] for the lanes of `live`; one atomic when the live lanes share a digit.
-__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t d, bool live, int lane) {
-  const unsigned m = __ballot_sync(0xffffffffu, live);
-  if (m == 0) return;
-  const int lead = __ffs(m) - 1;
-  const uint32_t d0 = __shfl_sync(0xffffffffu, d, lead);
-  if (__all_sync(0xffffffffu, !live || d == d0)) {
-    if (lane == lead) atomicAdd(&hist[d0], static_cast<uint32_t>(__popc(m)));
-  } else if (live) {
-    atomicAdd(&hist[d], 1u);
-  }
-}
-
 template <int C>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
     kv_evict_kernel(const __grid_constant__ EvictParams P) {
@@ -140,6 +127,20 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t o = order_bits(__ldg(w + i));
     return (i < P.first || i >= must_from) ? kMust : o;
   };
+  // f of every entry's bits, in any order: the lane's share of the piece
+  auto each_key = [&](auto f) {
+    if (stored) {
+      const uint4* k4 = reinterpret_cast<const uint4*>(keys);
+      const int n4 = (i1 - i0) / 4;
+      for (int q = lane; q < n4; q += 32) {
+        const uint4 v = k4[q];
+        f(v.x), f(v.y), f(v.z), f(v.w);
+      }
+      if (lane < (i1 - i0) % 4) f(keys[4 * n4 + lane]);
+    } else {
+      for (int i = i0 + lane; i < i1; i += 32) f(bits_at(i));
+    }
+  };
   auto key_at = [&](int i) -> uint32_t { return stored ? keys[i - i0] : bits_at(i); };
   // first digit, while the bits are stored
   for (int i = i0; i < i1; i += 32 * kAhead) {
@@ -147,12 +148,13 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) o[k] = i + 32 * k + lane < i1 ? bits_at(i + 32 * k + lane) : 0u;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const bool live = i + 32 * k + lane < i1;
-      if (live && stored) keys[i + 32 * k + lane - i0] = o[k];
-      count_digit(S->hist, o[k] >> 21, live, lane);
-    }
+    for (int k = 0; k < kAhead; ++k)
+      if (i + 32 * k + lane < i1) {
+        if (stored) keys[i + 32 * k + lane - i0] = o[k];
+        atomicAdd(&S->hist[o[k] >> 21], 1u);
+      }
   }
+  __syncwarp();  // a lane reads the others' bits from here on
   uint32_t need = static_cast<uint32_t>(P.budget), prefix = 0;
   // pass p: digit of `width` bits at `shift`, over the entries that agree with the prefix above it
 #pragma unroll
@@ -161,11 +163,9 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
     if (p > 0) {
       const int above = p == 1 ? 21 : 10;
       const uint32_t digit_mask = p == 1 ? 2047u : 1023u;
-      for (int i = i0; i < i1; i += 32) {
-        const bool in = i + lane < i1;
-        const uint32_t o = in ? key_at(i + lane) : 0u;
-        count_digit(S->hist + p * kBins, (o >> shift) & digit_mask, in && (o >> above) == (prefix >> above), lane);
-      }
+      each_key([&](uint32_t o) {
+        if ((o >> above) == (prefix >> above)) atomicAdd(&S->hist[p * kBins + ((o >> shift) & digit_mask)], 1u);
+      });
     }
     if (C > 1) cluster_sync();
     else __syncthreads();
@@ -175,8 +175,9 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
     if (C > 1) {
 #pragma unroll
       for (int k = 0; k < C; ++k) {
-        c += ld_cluster_u32(&S->hist[p * kBins + hi], k);
-        a += ld_cluster_u32(&S->hist[p * kBins + hi - 1], k);
+        const uint2 v = ld_cluster_u32x2(&S->hist[p * kBins + hi - 1], k);
+        a += v.x;
+        c += v.y;
       }
     } else {
       c = S->hist[p * kBins + hi];
@@ -199,11 +200,14 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // counts of entries above and equal to the threshold
   uint32_t above = 0, equal = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t o = in ? key_at(i + lane) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, in && o > prefix));
-    equal += __popc(__ballot_sync(0xffffffffu, in && o == prefix));
+  each_key([&](uint32_t o) {
+    above += o > prefix ? 1u : 0u;
+    equal += o == prefix ? 1u : 0u;
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    above += __shfl_xor_sync(0xffffffffu, above, o);
+    equal += __shfl_xor_sync(0xffffffffu, equal, o);
   }
   if (lane == 0) {
     S->above[warp] = above;

@@ -759,8 +759,8 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
 
 // ---------------------------------------------------------------- routing
 template <int P>
-void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, size_t smem,
-                       cudaStream_t stream) {
+void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, cudaStream_t stream) {
+  const size_t smem = (size_t)rg::kWarps * std::max(R.E, 32 * P) * 4;
   if (R.softmax)
     rg::route_fast_kernel<P, true><<<grid, rg::kThreads, smem, stream>>>(R, F);
   else
@@ -774,11 +774,11 @@ void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, cudaStre
   while (F.L * R.groups > 32) F.L /= 2;
   F.P = (F.S + F.L - 1) / F.L;
   F.vec = F.P % 4 == 0 && F.S == F.L * F.P && F.L * R.groups == 32 && (F.P & (F.P - 1)) == 0;
-  if (F.P <= 1) launch_route_fast<1>(R, F, grid, smem, stream);
-  else if (F.P <= 2) launch_route_fast<2>(R, F, grid, smem, stream);
-  else if (F.P <= 4) launch_route_fast<4>(R, F, grid, smem, stream);
-  else if (F.P <= 8) launch_route_fast<8>(R, F, grid, smem, stream);
-  else if (F.P <= 16) launch_route_fast<16>(R, F, grid, smem, stream);
+  if (F.P <= 1) launch_route_fast<1>(R, F, grid, stream);
+  else if (F.P <= 2) launch_route_fast<2>(R, F, grid, stream);
+  else if (F.P <= 4) launch_route_fast<4>(R, F, grid, stream);
+  else if (F.P <= 8) launch_route_fast<8>(R, F, grid, stream);
+  else if (F.P <= 16) launch_route_fast<16>(R, F, grid, stream);
   else rg::route_grouped_kernel<<<grid, rg::kThreads, smem, stream>>>(R);  // e.g. 17 groups of 30
 }
 

@@ -211,18 +211,20 @@ __device__ __forceinline__ float as_float(int k) { return __uint_as_float(static
 
 constexpr int kNone = static_cast<int>(0x80000000u);  // below every key (as a float -0)
 constexpr int kInf = 0x7F800000;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// The exact keys of the experts within `margin` of the k-th approximate one, ranked.  key: the lane's sorted
-// keys.  Returns false when there are more than 32 of them.
+// The exact keys of the experts within `margin` of the k-th approximate one, ranked.  sorted[32 m + lane]: the
+// lane's m-th largest key.  Returns false when there are more than 32 of them.
 template <int P>
 __device__ __noinline__ bool route_candidates(const RouteParams& R, const FastShape& F, int64_t tok, int lane,
-                                              const int* sorted, int mask, float margin) {
+                                              const int* sorted, float margin) {
+  constexpr int mask = P - 1;
   const float* x = R.logits + tok * R.E;
   int at = 0, n = 0, mine = 0;  // the lane's next key; candidates; this lane's candidate
   float cut = -INFINITY;
 #pragma unroll 1
   while (true) {
-    const int a = at < P ? sorted[at] : kNone;
+    const int a = at < P ? sorted[32 * at + lane] : kNone;
     const int M = __reduce_max_sync(0xffffffffu, a);
     if (M < 0 || as_float(M) < cut) break;
     if (n == 32) return false;
@@ -266,12 +268,13 @@ __device__ __noinline__ void route_exact_call(const RouteParams& R, int64_t tok,
 }
 
 template <int P, bool kSoftmax>
-__global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_constant__ RouteParams R,
+__global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) route_fast_kernel(const __grid_constant__ RouteParams R,
                                                               const __grid_constant__ FastShape F) {
-  extern __shared__ __align__(16) float sm[];  // E keys per warp (route_exact)
+  extern __shared__ __align__(16) float sm[];  // per warp: E keys (route_exact) or 32 P sorted ones
   constexpr int kMask = P - 1;                 // low bits of a key: P - 1 - place in the lane
   constexpr int kDepth = P < 4 ? P : 4;        // keys of a lane that the fast path can take
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* s_key = sm + warp * (32 * P > R.E ? 32 * P : R.E);
   const int g = lane / F.L, in_group = (lane % F.L) * F.P;
   const int count = g < R.groups ? max(0, min(F.P, F.S - in_group)) : 0;
   const int e0 = count > 0 ? g * F.S + in_group : 0;
@@ -326,17 +329,17 @@ __global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_const
       float sum = 0.f;
 #pragma unroll
       for (int m = 0; m < P; ++m) {
-        sc[m] = __expf(sc[m] - mx);
+        sc[m] = ex2_approx((sc[m] - mx) * kLog2e);
         sum += sc[m];
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      inv = __fdividef(1.f, sum);
+      inv = rcp_approx(sum);
 #pragma unroll
       for (int m = 0; m < P; ++m) sc[m] *= inv;
     } else {
 #pragma unroll
-      for (int m = 0; m < P; ++m) sc[m] = nb::route_sigmoid_approx(sc[m]);
+      for (int m = 0; m < P; ++m) sc[m] = rcp_approx(1.f + ex2_approx(sc[m] * -kLog2e));
     }
     int key[P];
 #pragma unroll
@@ -345,10 +348,12 @@ __global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_const
       key[m] = m < count ? (k & ~kMask) | (P - 1 - m) : kNone;
     }
     sort_desc<P>(key);
-    // A bound on twice the error of a key: the approximate sigmoid's 2^-21 (neighbors.cuh); for softmax, with
-    // d = max - x, exp's (2 + 1.173 d) 2^-23, the sum's the same averaged over the scores (d below ln 512
-    // there) and the division's, under 2^-18 of the score; the place in the low bits, at most 15 2^-23 of the
-    // key; FP32 roundings of the score, the bias's move and the sums.
+    // A bound on twice the error of a key.  2^y is within 2 ulp and its exponent rounded twice, so exp(-x) is
+    // within (2 + 2 |x|) 2^-23 and the sigmoid, with 1 / y within 1 ulp, within 2^-21 (exp's error reaches it
+    // times at most e^-|x|); for softmax, with d = max - x, (2 + 2 d) 2^-23 of the score, the sum's the same
+    // averaged over the scores (d below ln 512 there) and the reciprocal's: under 2^-18 of the score up to d = 12,
+    // and past that the score is below 2^-17 of the largest.  Then the place in the low bits, at most 15 2^-23
+    // of the key, and FP32 roundings of the score, the bias's move and the sums.
     const int top = __reduce_max_sync(0xffffffffu, key[0]);
     const float margin = (kSoftmax ? 0.f : 0x1p-19f) + 0x1p-16f * (as_float(top) + off);
     bool slow = top >= kInf;
@@ -360,15 +365,15 @@ __global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_const
         a = fmaxf(a, a2);
       }
       const float gs = F.S > 1 ? a + b : a;
-      int rank = 0;
-      for (int j = 0; j < R.groups; ++j) {  // exactly top_groups are kept
-        const float o = __shfl_sync(0xffffffffu, gs, j * F.L);
-        rank += (o > gs || (o == gs && j < g)) ? 1 : 0;
+      // the lower group ahead in the low bits (31 2^-23 of the score), so that exactly top_groups are kept
+      const int mine = g < R.groups ? (static_cast<int>(__float_as_uint(gs)) & ~31) | (31 - g) : kNone;
+      int left = mine, least = 0;
+      for (int j = 0; j < R.top_groups; ++j) {
+        least = __reduce_max_sync(0xffffffffu, left);
+        left = left == least ? kNone : left;
       }
-      const bool kept = rank < R.top_groups;
-      const int bits = static_cast<int>(__float_as_uint(gs));
-      const int least = __reduce_min_sync(0xffffffffu, g < R.groups && kept ? bits : 0x7FFFFFFF);
-      const int most = max(0, __reduce_max_sync(0xffffffffu, g < R.groups && !kept ? bits : 0));
+      const int most = max(0, __reduce_max_sync(0xffffffffu, left));
+      const bool kept = mine >= least;
       slow = slow || least < 0 || !(as_float(least) - as_float(most) > 2.f * margin);
       if (!kept) {
 #pragma unroll
@@ -410,22 +415,27 @@ __global__ void __launch_bounds__(kThreads) route_fast_kernel(const __grid_const
       }
       if (!__any_sync(0xffffffffu, unsure)) {
         float s = 0.f;
-        if (lane < R.top_k) s = kSoftmax ? expf(x - mx) * inv : __fdiv_rn(1.f, 1.f + expf(-x));
+        if (lane < R.top_k) s = kSoftmax ? expf(x - mx) * inv : rcp_approx(1.f + expf(-x));
         if (R.normalize) {
           float total = s;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-          s = __fdiv_rn(s, total);
+          s *= rcp_approx(total);
         }
         if (lane < R.top_k) {
           R.ids[tok * R.top_k + lane] = id;
           R.weights[tok * R.top_k + lane] = s * R.scale;
         }
       } else {
-        slow = !route_candidates<P>(R, F, tok, lane, key, kMask, margin);
+        int* sorted = reinterpret_cast<int*>(s_key);
+#pragma unroll
+        for (int m = 0; m < P; ++m) sorted[32 * m + lane] = key[m];
+        __syncwarp();
+        slow = !route_candidates<P>(R, F, tok, lane, sorted, margin);
+        __syncwarp();
       }
     }
-    if (slow) route_exact_call(R, tok, lane, sm + warp * R.E);
+    if (slow) route_exact_call(R, tok, lane, s_key);
   }
 }
 

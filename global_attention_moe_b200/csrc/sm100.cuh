@@ -370,6 +370,14 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
 }
+// The two 32-bit words that CTA `rank` of the cluster has where this CTA's shared memory has p (8-byte aligned).
+__device__ __forceinline__ uint2 ld_cluster_u32x2(const uint32_t* p, int rank) {
+  uint32_t a;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
 // The 32-bit word that CTA `rank` of the cluster has where this CTA's shared memory has *p.
 __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, int rank) {
   uint32_t a, v;
@@ -435,6 +443,13 @@ __device__ __forceinline__ void red_add_f32x4(float* p, float a, float b, float 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / x within 1 ulp; results below the normal range are 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 

@@ -551,4 +551,12 @@ inline uint32_t ld_cluster_u32(const uint32_t* p, int rank) {
   return v;
 }
 
+inline uint2 ld_cluster_u32x2(const uint32_t* p, int rank) {
+  return make_uint2(ld_cluster_u32(p, rank), ld_cluster_u32(p + 1, rank));
+}
+inline float rcp_approx(float x) {
+  const float y = 1.f / x;
+  return std::fabs(y) < 1.17549435e-38f ? std::copysign(0.f, y) : y;
+}
+
 }  // namespace mimo
