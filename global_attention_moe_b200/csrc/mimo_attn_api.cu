@@ -761,19 +761,26 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
 template <int P>
 void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, cudaStream_t stream) {
   const size_t smem = (size_t)rg::kWarps * std::max(R.E, 32 * P) * 4;
-  if (R.softmax)
-    rg::route_fast_kernel<P, true><<<grid, rg::kThreads, smem, stream>>>(R, F);
-  else
-    rg::route_fast_kernel<P, false><<<grid, rg::kThreads, smem, stream>>>(R, F);
+  const bool full = F.P == P && F.S == (F.P << F.lg) && (R.groups << F.lg) == 32;
+  if (R.softmax) {
+    if (full)
+      rg::route_fast_kernel<P, true, true><<<grid, rg::kThreads, smem, stream>>>(R, F);
+    else
+      rg::route_fast_kernel<P, true, false><<<grid, rg::kThreads, smem, stream>>>(R, F);
+  } else {
+    if (full)
+      rg::route_fast_kernel<P, false, true><<<grid, rg::kThreads, smem, stream>>>(R, F);
+    else
+      rg::route_fast_kernel<P, false, false><<<grid, rg::kThreads, smem, stream>>>(R, F);
+  }
 }
 
 void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, cudaStream_t stream) {
   rg::FastShape F;
   F.S = R.E / R.groups;
-  F.L = 32;
-  while (F.L * R.groups > 32) F.L /= 2;
-  F.P = (F.S + F.L - 1) / F.L;
-  F.vec = F.P % 4 == 0 && F.S == F.L * F.P && F.L * R.groups == 32 && (F.P & (F.P - 1)) == 0;
+  F.lg = 5;
+  while ((R.groups << F.lg) > 32) --F.lg;
+  F.P = (F.S + (1 << F.lg) - 1) >> F.lg;
   if (F.P <= 1) launch_route_fast<1>(R, F, grid, stream);
   else if (F.P <= 2) launch_route_fast<2>(R, F, grid, stream);
   else if (F.P <= 4) launch_route_fast<4>(R, F, grid, stream);

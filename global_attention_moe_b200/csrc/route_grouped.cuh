@@ -20,9 +20,10 @@
 //   3. top_k times, the warp's largest first key (one integer reduction) is taken from its lane;
 //   4. where every two neighbours of the k + 1 largest differ by more than twice the error bound, their
 //      order is that of the exact keys: the chosen experts' scores are formed in FP32 and written.
-// Otherwise the experts within the bound of the k-th key (at most 32) take their exact keys in FP64 and are
-// ranked; and where that does not decide either (group scores within the bound, more than 32 candidates,
-// keys that are NaN, infinite or far below the others), route_exact states the definition.
+// Other tokens are marked in ids and taken up after the loop, whose registers then hold no call: the experts
+// within the bound of the k-th key (at most 32) take their exact keys in FP64 and are ranked; and where that
+// does not decide either (group scores within the bound, more than 32 candidates, keys that are NaN,
+// infinite or far below the others), route_exact states the definition.
 #pragma once
 
 #include <stdint.h>
@@ -184,9 +185,9 @@ __global__ void __launch_bounds__(kThreads) route_grouped_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------- the fast kernel
-// What the lanes hold: S = E / groups experts to a group, L lanes to a group, P experts to a lane.
+// What the lanes hold: S = E / groups experts to a group, L = 2^lg lanes to a group, P experts to a lane.
 struct FastShape {
-  int S, L, P, vec;  // vec: every lane holds exactly P experts, a multiple of 4
+  int S, lg, P;
 };
 
 // Descending compare-exchange network (Batcher's odd-even merge sort), N a power of two.
@@ -213,51 +214,177 @@ constexpr int kNone = static_cast<int>(0x80000000u);  // below every key (as a f
 constexpr int kInf = 0x7F800000;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The exact keys of the experts within `margin` of the k-th approximate one, ranked.  sorted[32 m + lane]: the
-// lane's m-th largest key.  Returns false when there are more than 32 of them.
+// A lane's experts (e0 .. e0 + count - 1, count <= P) and their biases, moved up by the least of them (those
+// far below all others aside) so that keys are positive; `most` bounds the moved biases' size and the move.
 template <int P>
+struct Lane {
+  int g, e0, count;
+  float bias[P];
+  float most;
+  __device__ __forceinline__ Lane(const RouteParams& R, const FastShape& F, int lane) {
+    g = lane >> F.lg;
+    const int in_group = (lane & ((1 << F.lg) - 1)) * F.P;
+    count = g < R.groups ? max(0, min(F.P, F.S - in_group)) : 0;
+    e0 = count > 0 ? g * F.S + in_group : 0;
+    most = 0.f;
+#pragma unroll
+    for (int m = 0; m < P; ++m) bias[m] = 0.f;
+    if (R.bias == nullptr) return;
+    float low = INFINITY;
+#pragma unroll
+    for (int m = 0; m < P; ++m)
+      if (m < count) {
+        bias[m] = __ldg(R.bias + e0 + m);
+        if (bias[m] > -1024.f) low = fminf(low, bias[m]);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    if (!(fabsf(low) < 1e30f)) low = 0.f;
+    float high = 0.f;
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      bias[m] -= low;
+      high = fmaxf(high, bias[m]);
+    }
+    most = warp_max(high) + fabsf(low);
+  }
+  template <bool kFull>
+  __device__ __forceinline__ void load(const RouteParams& R, int64_t tok, float (&x)[P]) const {
+    const float* p = R.logits + tok * R.E + e0;
+    const bool in = tok < R.T;
+    if (kFull && P >= 4) {
+#pragma unroll
+      for (int m = 0; m < P / 4; ++m) {
+        const float4 v = in ? __ldg(reinterpret_cast<const float4*>(p) + m) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * m] = v.x, x[4 * m + 1] = v.y, x[4 * m + 2] = v.z, x[4 * m + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < P; ++m) x[m] = in && (kFull || m < count) ? __ldg(p + m) : -INFINITY;
+    }
+  }
+  // The approximate keys of logits x, sorted, their places in the low bits; and a bound on twice their error.
+  // 2^y is within 2 ulp and its exponent rounded twice, so exp(-x) is within (2 + 2 |x|) 2^-23 and the
+  // sigmoid, with 1 / y within 1 ulp, within 2^-21 (exp's error reaches it times at most e^-|x|); for softmax,
+  // with d = max - x, (2 + 2 d) 2^-23 of the score, the sum's the same averaged over the scores (d below
+  // ln 512 there) and the reciprocal's: under 2^-18 of the score up to d = 12, and past that the score is
+  // below 2^-17 of the largest.  Then the place in the low bits, at most 15 2^-23 of the key, and FP32
+  // roundings of the score, the bias's move and the sums.  mx and inv: softmax's maximum and 1 / sum.
+  template <bool kSoftmax, bool kFull>
+  __device__ __forceinline__ float keys(float (&x)[P], int (&key)[P], float& mx, float& inv) const {
+    mx = 0.f;
+    inv = 1.f;
+    if (kSoftmax) {
+      mx = x[0];
+#pragma unroll
+      for (int m = 1; m < P; ++m) mx = fmaxf(mx, x[m]);
+      mx = warp_max(mx);
+      float sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < P; ++m) {
+        x[m] = ex2_approx((x[m] - mx) * kLog2e);
+        sum += x[m];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      inv = rcp_approx(sum);
+#pragma unroll
+      for (int m = 0; m < P; ++m) x[m] = fmaf(x[m], inv, bias[m]);
+    } else {
+#pragma unroll
+      for (int m = 0; m < P; ++m) x[m] = rcp_approx(1.f + ex2_approx(x[m] * -kLog2e)) + bias[m];
+    }
+#pragma unroll
+    for (int m = 0; m < P; ++m) {
+      const int k = (static_cast<int>(__float_as_uint(x[m])) & ~(P - 1)) | (P - 1 - m);
+      key[m] = kFull || m < count ? k : kNone;
+    }
+    sort_desc<P>(key);
+    return kSoftmax ? 0x1p-16f * (inv + most) : 0x1p-19f + 0x1p-16f * (1.f + most);
+  }
+};
+
+// Which groups are kept, by the lanes' first two keys: false when the scores at the border are within the
+// error.  kept: whether this lane's is.
+template <int P>
+__device__ __forceinline__ bool choose_groups(const RouteParams& R, const FastShape& F, const int (&key)[P], int g,
+                                              float margin, bool& kept) {
+  float a = as_float(key[0]), b = P > 1 ? as_float(key[P > 1 ? 1 : 0]) : -0.f;
+#pragma unroll 1
+  for (int o = 1; o < (1 << F.lg); o <<= 1) {
+    const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+    b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+    a = fmaxf(a, a2);
+  }
+  const float gs = F.S > 1 ? a + b : a;
+  // the lower group ahead in the low bits (31 2^-23 of the score), so that exactly top_groups are kept
+  const int mine = g < R.groups ? (static_cast<int>(__float_as_uint(gs)) & ~31) | (31 - g) : kNone;
+  int left = mine, least = 0;
+#pragma unroll 4
+  for (int j = 0; j < R.top_groups; ++j) {
+    least = __reduce_max_sync(0xffffffffu, left);
+    left = left == least ? kNone : left;
+  }
+  const int most = max(0, __reduce_max_sync(0xffffffffu, left));
+  kept = mine >= least;
+  return least >= 0 && as_float(least) - as_float(most) > 2.f * margin;
+}
+
+// A token that the fast path left: the exact keys of the experts within the error of the k-th approximate
+// one, ranked.  Returns false when that does not decide: group scores at the border within the error, over 32
+// candidates, keys that are not ordinary numbers.  s_key: 32 P words of the warp's.
+template <int P, bool kSoftmax>
 __device__ __noinline__ bool route_candidates(const RouteParams& R, const FastShape& F, int64_t tok, int lane,
-                                              const int* sorted, float margin) {
-  constexpr int mask = P - 1;
-  const float* x = R.logits + tok * R.E;
-  int at = 0, n = 0, mine = 0;  // the lane's next key; candidates; this lane's candidate
+                                              int* s_key) {
+  const Lane<P> mine(R, F, lane);
+  float v[P], mx, inv;
+  int key[P];
+  mine.template load<false>(R, tok, v);
+  const float margin = mine.template keys<kSoftmax, false>(v, key, mx, inv);
+  if (__any_sync(0xffffffffu, key[0] >= kInf)) return false;
+  bool kept = true;
+  if (R.top_groups < R.groups && !choose_groups<P>(R, F, key, mine.g, margin, kept)) return false;
+#pragma unroll
+  for (int m = 0; m < P; ++m) s_key[32 * m + lane] = kept ? key[m] : kNone;
+  __syncwarp();
+  int at = 0, n = 0, e = 0;  // the lane's next key; candidates; this lane's candidate
   float cut = -INFINITY;
 #pragma unroll 1
   while (true) {
-    const int a = at < P ? sorted[32 * at + lane] : kNone;
+    const int a = at < P ? s_key[32 * at + lane] : kNone;
     const int M = __reduce_max_sync(0xffffffffu, a);
     if (M < 0 || as_float(M) < cut) break;
     if (n == 32) return false;
     const int first = __ffs(__ballot_sync(0xffffffffu, a == M)) - 1;
     if (lane == first) ++at;
-    if (lane == n) mine = (first / F.L) * F.S + (first % F.L) * F.P + (P - 1 - (M & mask));
+    const int e1 = __shfl_sync(0xffffffffu, mine.e0, first) + P - 1 - (M & (P - 1));
+    if (lane == n) e = e1;
     if (++n == R.top_k) cut = as_float(M) - margin;
   }
   if (n < R.top_k) return false;
+  const float* x = R.logits + tok * R.E;
   double sc = 0.0;
-  if (R.softmax) {
-    float mx = -INFINITY;
-    for (int e = lane; e < R.E; e += 32) mx = fmaxf(mx, __ldg(x + e));
-    const double m = static_cast<double>(warp_max(mx));
+  if (kSoftmax) {
+    const double m = static_cast<double>(mx);
     double S = 0.0;
-    for (int e = lane; e < R.E; e += 32) S += exp(static_cast<double>(__ldg(x + e)) - m);
+    for (int i = lane; i < R.E; i += 32) S += exp(static_cast<double>(__ldg(x + i)) - m);
     S = warp_sum_f64(S);
-    sc = exp(static_cast<double>(__ldg(x + mine)) - m) / S;
+    sc = exp(static_cast<double>(__ldg(x + e)) - m) / S;
   } else {
-    sc = nb::route_sigmoid_f64(static_cast<double>(__ldg(x + mine)));
+    sc = nb::route_sigmoid_f64(static_cast<double>(__ldg(x + e)));
   }
-  const float key = static_cast<float>(sc) + (R.bias != nullptr ? __ldg(R.bias + mine) : 0.f);
+  const float exact = static_cast<float>(sc) + (R.bias != nullptr ? __ldg(R.bias + e) : 0.f);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
-    const float o = __shfl_sync(0xffffffffu, key, j);
-    const int e = __shfl_sync(0xffffffffu, mine, j);
-    rank += (o > key || (o == key && e < mine)) ? 1 : 0;
+    const float o = __shfl_sync(0xffffffffu, exact, j);
+    const int i = __shfl_sync(0xffffffffu, e, j);
+    rank += (o > exact || (o == exact && i < e)) ? 1 : 0;
   }
   const bool chosen = lane < n && rank < R.top_k;
   const double total = warp_sum_f64(chosen ? sc : 0.0);
   if (chosen) {
     const double w = R.normalize ? (total == 0.0 ? 0.0 : sc / total) : sc;
-    R.ids[tok * R.top_k + rank] = mine;
+    R.ids[tok * R.top_k + rank] = e;
     R.weights[tok * R.top_k + rank] = static_cast<float>(w * static_cast<double>(R.scale));
   }
   return true;
@@ -267,153 +394,63 @@ __device__ __noinline__ void route_exact_call(const RouteParams& R, int64_t tok,
   route_exact(R, tok, lane, s_key);
 }
 
-template <int P, bool kSoftmax>
+template <int P, bool kSoftmax, bool kFull>  // kFull: every lane holds exactly P experts
 __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) route_fast_kernel(const __grid_constant__ RouteParams R,
-                                                              const __grid_constant__ FastShape F) {
-  extern __shared__ __align__(16) float sm[];  // per warp: E keys (route_exact) or 32 P sorted ones
-  constexpr int kMask = P - 1;                 // low bits of a key: P - 1 - place in the lane
-  constexpr int kDepth = P < 4 ? P : 4;        // keys of a lane that the fast path can take
+                                                                              const __grid_constant__ FastShape F) {
+  extern __shared__ __align__(16) float sm[];    // per warp: E keys (route_exact) or 32 P sorted ones
+  __shared__ int2 s_pick[kWarps][32];            // the largest keys in turn, and the lanes that held them
+  constexpr int kDepth = P < 4 ? P : 4;          // keys of a lane that the fast path can take
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* s_key = sm + warp * (32 * P > R.E ? 32 * P : R.E);
-  const int g = lane / F.L, in_group = (lane % F.L) * F.P;
-  const int count = g < R.groups ? max(0, min(F.P, F.S - in_group)) : 0;
-  const int e0 = count > 0 ? g * F.S + in_group : 0;
-  // biases moved up by the least of them (those far below all others aside), so that keys are positive
-  float bl[P], low = 0.f;
-#pragma unroll
-  for (int m = 0; m < P; ++m) bl[m] = 0.f;
-  if (R.bias != nullptr) {
-    low = INFINITY;
-#pragma unroll
-    for (int m = 0; m < P; ++m)
-      if (m < count) {
-        bl[m] = __ldg(R.bias + e0 + m);
-        if (bl[m] > -1024.f) low = fminf(low, bl[m]);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-    if (!(fabsf(low) < 1e30f)) low = 0.f;
-#pragma unroll
-    for (int m = 0; m < P; ++m) bl[m] -= low;
-  }
-  const float off = fabsf(low);
+  int2* pick = s_pick[warp];
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  float xn[P];  // the next token's logits
-  auto load = [&](int64_t t) {
-    if (P >= 4 && F.vec) {
-      const float4* p = reinterpret_cast<const float4*>(R.logits + t * R.E + e0);
-#pragma unroll
-      for (int m = 0; m < P / 4; ++m) {
-        const float4 v = t < R.T ? __ldg(p + m) : make_float4(0.f, 0.f, 0.f, 0.f);
-        xn[4 * m] = v.x, xn[4 * m + 1] = v.y, xn[4 * m + 2] = v.z, xn[4 * m + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < P; ++m) xn[m] = t < R.T && m < count ? __ldg(R.logits + t * R.E + e0 + m) : -INFINITY;
-    }
-  };
-  load(tok);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  {
+    const Lane<P> mine(R, F, lane);
+    float xn[P];  // the next token's logits
+    mine.template load<kFull>(R, first, xn);
 #pragma unroll 1
-  for (; tok < R.T; tok += step) {
-    float sc[P];
+    for (int64_t tok = first; tok < R.T; tok += step) {
+      float v[P], mx, inv;
 #pragma unroll
-    for (int m = 0; m < P; ++m) sc[m] = xn[m];
-    load(tok + step);  // in flight meanwhile
-    float mx = 0.f, inv = 1.f;
-    if (kSoftmax) {
-      mx = sc[0];
-#pragma unroll
-      for (int m = 1; m < P; ++m) mx = fmaxf(mx, sc[m]);
-      mx = warp_max(mx);
-      float sum = 0.f;
-#pragma unroll
-      for (int m = 0; m < P; ++m) {
-        sc[m] = ex2_approx((sc[m] - mx) * kLog2e);
-        sum += sc[m];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      inv = rcp_approx(sum);
-#pragma unroll
-      for (int m = 0; m < P; ++m) sc[m] *= inv;
-    } else {
-#pragma unroll
-      for (int m = 0; m < P; ++m) sc[m] = rcp_approx(1.f + ex2_approx(sc[m] * -kLog2e));
-    }
-    int key[P];
-#pragma unroll
-    for (int m = 0; m < P; ++m) {
-      const int k = static_cast<int>(__float_as_uint(sc[m] + bl[m]));
-      key[m] = m < count ? (k & ~kMask) | (P - 1 - m) : kNone;
-    }
-    sort_desc<P>(key);
-    // A bound on twice the error of a key.  2^y is within 2 ulp and its exponent rounded twice, so exp(-x) is
-    // within (2 + 2 |x|) 2^-23 and the sigmoid, with 1 / y within 1 ulp, within 2^-21 (exp's error reaches it
-    // times at most e^-|x|); for softmax, with d = max - x, (2 + 2 d) 2^-23 of the score, the sum's the same
-    // averaged over the scores (d below ln 512 there) and the reciprocal's: under 2^-18 of the score up to d = 12,
-    // and past that the score is below 2^-17 of the largest.  Then the place in the low bits, at most 15 2^-23
-    // of the key, and FP32 roundings of the score, the bias's move and the sums.
-    const int top = __reduce_max_sync(0xffffffffu, key[0]);
-    const float margin = (kSoftmax ? 0.f : 0x1p-19f) + 0x1p-16f * (as_float(top) + off);
-    bool slow = top >= kInf;
-    if (R.top_groups < R.groups) {
-      float a = as_float(key[0]), b = P > 1 ? as_float(key[P > 1 ? 1 : 0]) : -0.f;
-      for (int o = 1; o < F.L; o <<= 1) {
-        const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
-        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
-        a = fmaxf(a, a2);
-      }
-      const float gs = F.S > 1 ? a + b : a;
-      // the lower group ahead in the low bits (31 2^-23 of the score), so that exactly top_groups are kept
-      const int mine = g < R.groups ? (static_cast<int>(__float_as_uint(gs)) & ~31) | (31 - g) : kNone;
-      int left = mine, least = 0;
-      for (int j = 0; j < R.top_groups; ++j) {
-        least = __reduce_max_sync(0xffffffffu, left);
-        left = left == least ? kNone : left;
-      }
-      const int most = max(0, __reduce_max_sync(0xffffffffu, left));
-      const bool kept = mine >= least;
-      slow = slow || least < 0 || !(as_float(least) - as_float(most) > 2.f * margin);
-      if (!kept) {
-#pragma unroll
-        for (int m = 0; m < P; ++m) key[m] = kNone;
-      }
-    }
-    if (!slow) {
+      for (int m = 0; m < P; ++m) v[m] = xn[m];
+      mine.template load<kFull>(R, tok + step, xn);  // in flight meanwhile
+      int key[P];
+      const float margin = mine.template keys<kSoftmax, kFull>(v, key, mx, inv);
+      bool sure = !__any_sync(0xffffffffu, key[0] >= kInf);
+      bool kept = true;
+      if (R.top_groups < R.groups) sure = choose_groups<P>(R, F, key, mine.g, margin, kept) && sure;
       int h[kDepth];
 #pragma unroll
-      for (int m = 0; m < kDepth; ++m) h[m] = key[m];
-      int M = 0;
-      unsigned from = 0;  // lane c: the c-th largest key and the lane it came from
-#pragma unroll 1
+      for (int m = 0; m < kDepth; ++m) h[m] = kept ? key[m] : kNone;
+      const int deep = P > kDepth && kept ? key[P > kDepth ? kDepth : 0] : kNone;
+      int taken = 0;
+      __syncwarp();  // the last token's picks are read
+#pragma unroll 4
       for (int c = 0; c < R.top_k; ++c) {
         const int best = __reduce_max_sync(0xffffffffu, h[0]);
-        const bool here = h[0] == best;
-        const unsigned who = __ballot_sync(0xffffffffu, here);
-        if (lane == c) {
-          M = best;
-          from = who;
-        }
+        if (h[0] == best) {
+          pick[c] = make_int2(best, lane);
+          ++taken;
 #pragma unroll
-        for (int m = 0; m + 1 < kDepth; ++m) h[m] = here ? h[m + 1] : h[m];
-        h[kDepth - 1] = here ? kNone : h[kDepth - 1];
+          for (int m = 0; m + 1 < kDepth; ++m) h[m] = h[m + 1];
+          h[kDepth - 1] = kNone;
+        }
       }
       const int next = __reduce_max_sync(0xffffffffu, h[0]);
-      const int after = __shfl_sync(0xffffffffu, M, lane + 1 < 32 ? lane + 1 : 31);
-      const float gap = as_float(M) - as_float(lane == R.top_k - 1 ? next : after);
-      const float kth = as_float(__shfl_sync(0xffffffffu, M, R.top_k - 1));
-      bool unsure = P > kDepth && as_float(key[P > kDepth ? kDepth : 0]) > kth - margin;
-      int id = 0;
+      const int count = __reduce_add_sync(0xffffffffu, taken);  // over top_k: one key in two lanes
+      __syncwarp();
+      const int2 own = lane < R.top_k ? pick[lane] : make_int2(0, 0);
+      const int after = lane + 1 < R.top_k ? pick[lane + 1].x : next;
+      const float kth = as_float(pick[R.top_k - 1].x);
+      sure = sure && count == R.top_k && !(P > kDepth && as_float(deep) > kth - margin);
+      const int e = __shfl_sync(0xffffffffu, mine.e0, own.y) + P - 1 - (own.x & (P - 1));
       float x = 0.f;
       if (lane < R.top_k) {
-        unsure = unsure || M < 0 || !(gap > margin) || __popc(from) != 1;
-        const int src = __ffs(from) - 1;
-        id = (src / F.L) * F.S + (src % F.L) * F.P + (P - 1 - (M & kMask));
-        if (!unsure) x = __ldg(R.logits + tok * R.E + id);
-        unsure = unsure || x - mx < -80.f;  // scores that FP32 may not hold
+        sure = sure && own.x >= 0 && as_float(own.x) - as_float(after) > margin;
+        if (sure) x = __ldg(R.logits + tok * R.E + e);
+        sure = sure && x - mx > -80.f;  // scores that FP32 holds
       }
-      if (!__any_sync(0xffffffffu, unsure)) {
+      if (__all_sync(0xffffffffu, sure)) {
         float s = 0.f;
         if (lane < R.top_k) s = kSoftmax ? expf(x - mx) * inv : rcp_approx(1.f + expf(-x));
         if (R.normalize) {
@@ -423,19 +460,29 @@ __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) route_fast_kernel(co
           s *= rcp_approx(total);
         }
         if (lane < R.top_k) {
-          R.ids[tok * R.top_k + lane] = id;
+          R.ids[tok * R.top_k + lane] = e;
           R.weights[tok * R.top_k + lane] = s * R.scale;
         }
-      } else {
-        int* sorted = reinterpret_cast<int*>(s_key);
-#pragma unroll
-        for (int m = 0; m < P; ++m) sorted[32 * m + lane] = key[m];
-        __syncwarp();
-        slow = !route_candidates<P>(R, F, tok, lane, sorted, margin);
-        __syncwarp();
+      } else if (lane == 0) {
+        R.ids[tok * R.top_k] = -1;  // left for below
       }
     }
-    if (slow) route_exact_call(R, tok, lane, s_key);
+  }
+  __syncwarp();
+  // the tokens of this warp that were left
+  float* s_key = sm + warp * (32 * P > R.E ? 32 * P : R.E);
+#pragma unroll 1
+  for (int64_t t0 = first; t0 < R.T; t0 += 32 * step) {
+    const int64_t t = t0 + lane * step;
+    unsigned left = __ballot_sync(0xffffffffu, t < R.T && *(R.ids + t * R.top_k) < 0);
+    for (; left; left &= left - 1) {
+      const int64_t tok = t0 + (__ffs(left) - 1) * step;
+      if (!route_candidates<P, kSoftmax>(R, F, tok, lane, reinterpret_cast<int*>(s_key))) {
+        __syncwarp();
+        route_exact_call(R, tok, lane, s_key);
+      }
+      __syncwarp();
+    }
   }
 }
 
