@@ -789,6 +789,24 @@ void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, cudaStre
   else rg::route_grouped_kernel<<<grid, rg::kThreads, smem, stream>>>(R);  // e.g. 17 groups of 30
 }
 
+void launch_route_bwd(const rg::RouteBwdParams& P, int sms, cudaStream_t stream) {
+  // places to a token: at least top_k, and rows of a warp's tokens that fit shared memory without asking
+  const int W = P.top_k <= 8 && P.E <= 384 ? 8 : P.top_k <= 16 ? 16 : 32;
+  const bool dense = P.softmax && !P.normalize;
+  const int per_warp = dense ? 1 : 32 / W;  // tokens
+  const long long blocks = (P.T + rg::kWarps * per_warp - 1) / (rg::kWarps * per_warp);
+  const unsigned grid = (unsigned)std::min<long long>(blocks, 32LL * sms);
+  const size_t smem = (size_t)rg::kWarps * ((per_warp * P.E + 3) / 4 * 4) * 4;
+  if (dense)
+    rg::route_bwd_dense_kernel<<<grid, rg::kThreads, 0, stream>>>(P);
+  else if (W == 8)
+    rg::route_bwd_sparse_kernel<8><<<grid, rg::kThreads, smem, stream>>>(P);
+  else if (W == 16)
+    rg::route_bwd_sparse_kernel<16><<<grid, rg::kThreads, smem, stream>>>(P);
+  else
+    rg::route_bwd_sparse_kernel<32><<<grid, rg::kThreads, smem, stream>>>(P);
+}
+
 // ---------------------------------------------------------------- eviction
 constexpr uint32_t kEvictMaxSmem = 200 * 1024;
 
@@ -1320,9 +1338,7 @@ int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const float* dwe
   P.softmax = score == MIMO_ROUTE_SOFTMAX;
   P.normalize = normalize != 0;
   P.scale = scale;
-  const unsigned grid = (unsigned)std::min<long long>((tokens + rg::kWarps - 1) / rg::kWarps, 16LL * info->sms);
-  const size_t smem = (size_t)rg::kWarps * num_experts * 4;
-  rg::route_bwd_kernel<<<grid, rg::kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
+  launch_route_bwd(P, info->sms, static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 

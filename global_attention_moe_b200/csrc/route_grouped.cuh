@@ -503,66 +503,173 @@ struct RouteBwdParams {
 //   sigmoid               dx_j = scale g_j s_j (1 - s_j)
 //   softmax, normalised   dx_j = scale (g_j - gm) p_j                (the softmax's own sum cancels)
 //   softmax               dx_e = scale s_e (sum of g_j with id_j = e - sum_j g_j s_j)     every expert
-// An id outside [0, E) is an empty place: it takes no part.  The same id twice adds up.
-// One warp per token; the row is put together in shared memory and written whole.
-__global__ void __launch_bounds__(kThreads) route_bwd_kernel(const __grid_constant__ RouteBwdParams P) {
-  extern __shared__ __align__(16) float sm[];  // E per warp
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = sm + warp * P.E;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + warp; tok < P.T; tok += step) {
-    const float* x = P.logits + tok * P.E;
+// An id outside [0, E) is an empty place: it takes no part.  The same id twice adds up, in the order of the
+// places.  p and the derivatives are formed in FP32 from e^-|x| (1 - s is formed as a score, not by
+// subtraction); a token whose chosen scores all fall below e^-60 takes FP64, where FP32 would lose them.
+//
+// Both kernels are bound by the rows they write.
+
+// The place's peers: the lanes with the same id (empty places: alone).  Returns, in every lane, the sum of v
+// over the peers in the order of the lanes, and whether this lane is the first of them.
+__device__ __forceinline__ float sum_same(float v, int tag, int lane, bool& lead) {
+  const unsigned peers = __match_any_sync(0xffffffffu, tag);
+  lead = __ffs(peers) - 1 == lane;
+  if (__all_sync(0xffffffffu, peers == (1u << lane))) return v;
+  float s = 0.f;
+  for (int j = 0; j < 32; ++j) {
+    const float o = __shfl_sync(0xffffffffu, v, j);
+    if ((peers >> j) & 1u) s += o;
+  }
+  return s;
+}
+
+// d w_j / d x_j times g, less the means, for W places of a token in W lanes, in FP64 (few tokens).
+template <int W>
+__device__ __noinline__ float bwd_place_f64(int softmax, int normalize, float g, float x, bool has) {
+  auto sum = [](double v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  const double xd = static_cast<double>(x), gd = static_cast<double>(g);
+  double s = 0.0, c = 1.0;
+  if (softmax) {
+    double mx = has ? xd : -INFINITY;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    s = has && mx > -INFINITY ? exp(xd - mx) : 0.0;
+  } else if (has) {
+    s = nb::route_sigmoid_f64(xd);
+    c = nb::route_sigmoid_f64(-xd);
+  }
+  if (!normalize) return static_cast<float>(gd * s * c);
+  const double S = sum(s);
+  const double p = S == 0.0 ? 0.0 : s / S;
+  const double gm = sum(has ? gd * p : 0.0);
+  return static_cast<float>((gd - gm) * p * c);
+}
+
+// All but the plain softmax: few elements of a row are not zero.  W lanes to a token (top_k <= W), 32 / W
+// tokens to a warp; the rows are put together in shared memory, which is zero between uses, and written
+// whole with 16-byte stores.
+template <int W>
+__global__ void __launch_bounds__(kThreads) route_bwd_sparse_kernel(const __grid_constant__ RouteBwdParams P) {
+  constexpr int kTokens = 32 / W;
+  extern __shared__ __align__(16) float sm[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / W, j = lane % W;
+  float* rows = sm + warp * ((kTokens * P.E + 3) & ~3);
+  const int n = kTokens * P.E;
+  for (int e = lane; e < n; e += 32) rows[e] = 0.f;
+  __syncwarp();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens; t0 < P.T; t0 += step) {
+    const int64_t tok = t0 + sub;
     int id = -1;
-    double g = 0.0;
-    if (lane < P.top_k) {
-      id = __ldg(P.ids + tok * P.top_k + lane);
+    float g = 0.f, x = -INFINITY;
+    if (tok < P.T && j < P.top_k) {
+      id = __ldg(P.ids + tok * P.top_k + j);
+      g = __ldg(P.dweights + tok * P.top_k + j) * P.scale;
       if (id < 0 || id >= P.E) id = -1;
-      if (id >= 0) g = static_cast<double>(P.scale) * static_cast<double>(__ldg(P.dweights + tok * P.top_k + lane));
+      if (id >= 0) x = __ldg(P.logits + tok * P.E + id);
+      else g = 0.f;
     }
-    const double xj = id >= 0 ? static_cast<double>(__ldg(x + id)) : -INFINITY;
-    for (int e = lane; e < P.E; e += 32) row[e] = 0.f;
-    __syncwarp();
-    double d = 0.0;  // this place's share of dx[id]
-    if (!P.softmax) {
-      const double s = id >= 0 ? nb::route_sigmoid_f64(xj) : 0.0, c = id >= 0 ? nb::route_sigmoid_f64(-xj) : 0.0;
+    const bool has = id >= 0;
+    auto sum = [](float v) {
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    float mx = x;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float d;
+    if (__any_sync(0xffffffffu, has && !P.softmax && !(mx > -60.f))) {  // NaN too
+      d = bwd_place_f64<W>(P.softmax, P.normalize, g, x, has);
+    } else {
+      float s, c = 1.f;
+      if (P.softmax) {
+        s = has && mx > -INFINITY ? expf(x - mx) : 0.f;
+      } else {
+        const float e = expf(-fabsf(x)), r = __fdiv_rn(1.f, 1.f + e);
+        s = has ? (x >= 0.f ? r : e * r) : 0.f;
+        c = x >= 0.f ? e * r : r;
+        if (x != x) s = x;
+      }
       if (P.normalize) {
-        const double S = warp_sum_f64(s);
-        const double p = S == 0.0 ? 0.0 : s / S;
-        const double gm = warp_sum_f64(g * p);
-        d = (g - gm) * p * c;
+        const float S = sum(s);
+        const float p = S == 0.f ? 0.f : __fdiv_rn(s, S);
+        d = (g - sum(g * p)) * p * c;
       } else {
         d = g * s * c;
       }
-    } else if (P.normalize) {
-      double mx = xj;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const double s = id >= 0 && mx > -INFINITY ? exp(xj - mx) : 0.0;
-      const double S = warp_sum_f64(s);
-      const double p = S == 0.0 ? 0.0 : s / S;
-      const double gm = warp_sum_f64(g * p);
-      d = (g - gm) * p;
-    } else {
-      float mx = -INFINITY;
-      for (int e = lane; e < P.E; e += 32) mx = fmaxf(mx, __ldg(x + e));
-      const double m = static_cast<double>(warp_max(mx));
-      double S = 0.0;
-      for (int e = lane; e < P.E; e += 32) S += exp(static_cast<double>(__ldg(x + e)) - m);
-      S = warp_sum_f64(S);
-      const double s = id >= 0 ? exp(xj - m) / S : 0.0;
-      const double gm = warp_sum_f64(g * s);
-      for (int e = lane; e < P.E; e += 32)
-        row[e] = static_cast<float>(-gm * (exp(static_cast<double>(__ldg(x + e)) - m) / S));
-      __syncwarp();
-      d = g * s;
     }
-    // places in turn, so that the same id twice adds up in a fixed order
-    for (int j = 0; j < P.top_k; ++j) {
-      if (lane == j && id >= 0) row[id] += static_cast<float>(d);
-      __syncwarp();
-    }
-    for (int e = lane; e < P.E; e += 32) P.dlogits[tok * P.E + e] = row[e];
+    bool lead;
+    d = sum_same(d, has ? sub * P.E + id : -1 - lane, lane, lead);
+    float* at = rows + sub * P.E + id;
+    if (has && lead) *at = d;
     __syncwarp();
+    const int64_t left = (P.T - t0) * P.E;
+    float* out = P.dlogits + t0 * P.E;
+    if ((P.E & 3) == 0) {
+      const int m = static_cast<int>(min(static_cast<int64_t>(n), left)) / 4;
+      for (int e = lane; e < m; e += 32) reinterpret_cast<float4*>(out)[e] = reinterpret_cast<const float4*>(rows)[e];
+    } else {
+      const int m = static_cast<int>(min(static_cast<int64_t>(n), left));
+      for (int e = lane; e < m; e += 32) out[e] = rows[e];
+    }
+    __syncwarp();
+    if (has && lead) *at = 0.f;
+    __syncwarp();
+  }
+}
+
+// Softmax weights that were not renormalised: every element of the row.  One warp per token.
+__global__ void __launch_bounds__(kThreads) route_bwd_dense_kernel(const __grid_constant__ RouteBwdParams P) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); tok < P.T; tok += step) {
+    const float* x = P.logits + tok * P.E;
+    float v[kMaxPerLane];
+    int id = -1;
+    float g = 0.f, xj = -INFINITY;
+    if (lane < P.top_k) {
+      id = __ldg(P.ids + tok * P.top_k + lane);
+      g = __ldg(P.dweights + tok * P.top_k + lane) * P.scale;
+      if (id < 0 || id >= P.E) id = -1;
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int m = 0; m < kMaxPerLane; ++m)
+      if (32 * m < P.E) {
+        v[m] = lane + 32 * m < P.E ? __ldg(x + lane + 32 * m) : -INFINITY;
+        mx = fmaxf(mx, v[m]);
+      }
+    if (id >= 0) xj = __ldg(x + id);
+    else g = 0.f;
+    mx = warp_max(mx);
+    float S = 0.f;
+#pragma unroll
+    for (int m = 0; m < kMaxPerLane; ++m)
+      if (32 * m < P.E) {
+        v[m] = lane + 32 * m < P.E ? expf(v[m] - mx) : 0.f;
+        S += v[m];
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    const float inv = __fdiv_rn(1.f, S);
+    const float s = id >= 0 ? expf(xj - mx) * inv : 0.f;
+    float gm = g * s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) gm += __shfl_xor_sync(0xffffffffu, gm, o);
+    float* out = P.dlogits + tok * P.E;
+    const float f = -gm * inv;
+#pragma unroll
+    for (int m = 0; m < kMaxPerLane; ++m)
+      if (lane + 32 * m < P.E) out[lane + 32 * m] = f * v[m];
+    bool lead;
+    const float gs = sum_same(g, id >= 0 ? id : -1 - lane, lane, lead);
+    __syncwarp();  // the row's stores above come before those of the chosen experts
+    if (id >= 0 && lead) out[id] = s * (gs - gm);
   }
 }
 

@@ -400,6 +400,15 @@ inline unsigned __ballot_sync(unsigned, int pred) {
   hemu::syncwarp();
   return r;
 }
+inline unsigned __match_any_sync(unsigned, int v) {
+  const int l = hemu::lin_tid() % 32, w = hemu::warp_slot();
+  hemu::g_xch[w][l] = static_cast<uint32_t>(v);
+  hemu::syncwarp();
+  unsigned r = 0;
+  for (int i = 0; i < 32; ++i) r |= (static_cast<uint32_t>(hemu::g_xch[w][i]) == static_cast<uint32_t>(v) ? 1u : 0u) << i;
+  hemu::syncwarp();
+  return r;
+}
 template <class F>
 inline int hemu_reduce(int v, F f) {
   const int l = hemu::lin_tid() % 32, w = hemu::warp_slot();

@@ -266,7 +266,9 @@ CASES = {
         (4, 64, 4, False, False, 83, 0.5), (3, 60, 60 // 2, True, True, 84), (2, 512, 32, False, True, 85),
         (2, 1, 1, True, False, 86), (3, 7, 3, False, True, 87), (3, 160, 8, True, False, 88),
         (3, 256, 8, False, True, 89, 1.0, "far"), (3, 256, 8, True, True, 90, 1.0, "far"),
-        (3, 128, 8, True, False, 91, 1.0, "masked"), (3, 128, 8, False, True, 92, 1.0, "masked"))],
+        (3, 128, 8, True, False, 91, 1.0, "masked"), (3, 128, 8, False, True, 92, 1.0, "masked"),
+        (9, 512, 8, False, True, 93), (9, 384, 8, True, True, 94), (3, 160, 8, True, False, 96, 1.0, "far"), (5, 66, 12, False, True, 97),
+        (3, 64, 6, False, False, 98, 1.0, "far"), (33, 60, 5, False, True, 99))],
     "route_bwd_places": lambda be: route_bwd_places(be),
     "weights_step": lambda be: [check_weights(be, *c) for c in (
         ([5, 129, 300, 64], [1, 1, 1, 1], 8, 2, -1, 1e7, 100), ([130, 1, 257], [8, 1, 3], 8, 2, -1, 1e4, 101, False, True),
