@@ -24,16 +24,19 @@
 //      head][key];
 //   3. kw_join_kernel: adds the partial rows in a fixed order, and prev.
 //
-// Warp roles of the main kernel (14 warps):
+// Warp roles of the main kernel (18 warps):
 //   warps 0-3   sums (thread = key = TMEM lane)
 //   warps 4-7   K fetcher: gathers the tile's rows by index with cp.async into the 128-byte-swizzled layout
-//   warps 8-11  K rotation: BF16 -> FP16 hi in place, lo beside it (angle addition from the tile's start)
-//   warp 12     TMEM owner; lane 0 issues the MMAs
-//   warp 13     Q loader: TMA boxes of the prepared rows, and their lse
-// Units are walked in order by every role.  With one query tile per sequence (decode steps) a CTA takes a
-// contiguous run of units, so Q stays in shared memory while the keys of a (sequence, KV head) stream
-// through two K stages; with more (chunked prefill) the key tile stays while the query tiles stream
-// through two Q stages.
+//   warps 8-15  K rotation, two threads to a key: BF16 -> FP16 hi in place, lo into a buffer of its own
+//               (angle addition from the tile's first key; paired FP32 arithmetic)
+//   warp 16     TMEM owner; lane 0 issues the MMAs
+//   warp 17     Q loader: TMA boxes of the prepared rows, and their lse
+// Units are walked in order by every role.  K tiles go through a ring of KS stages (48 KB: hi, pass, pass), Q
+// tiles through a ring of QG granules of 128 rows x 64 dims (hi, lo, pass, pass of each tile in turn), each
+// handed back as soon as its products are done.  With one query tile per sequence (decode steps) a CTA takes a
+// contiguous run of units, so Q stays in its four granules while the keys of a (sequence, KV head) stream
+// through three stages; with more (chunked prefill) a key tile stays in one of two stages while the query
+// tiles stream through seven granules.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -42,14 +45,18 @@
 namespace mimo {
 namespace kw {
 
-constexpr int kThreads = 448;
-constexpr int kTile = 128;                 // keys per unit
-constexpr uint32_t kUnit = 16384;          // 128 rows x 64 dims x 2 B
-constexpr uint32_t kStage = 4 * kUnit;     // K: hi, pass, pass, lo; Q: hi, lo, pass, pass
-constexpr uint32_t kCtrlOff = 3 * kStage;  // two K stages and one Q stage, or one and two
+constexpr int kThreads = 576;
+constexpr int kTile = 128;             // keys per unit
+constexpr uint32_t kUnit = 16384;      // 128 rows x 64 dims x 2 B
+constexpr uint32_t kStage = 3 * kUnit;  // K: hi, pass, pass
+constexpr uint32_t kLoOff = 0;         // the rotated dims' low parts of one K tile
+constexpr uint32_t kRingOff = kUnit;   // KS stages, then QG granules: 13 units
+constexpr uint32_t kCtrlOff = 14 * kUnit;
 constexpr int kLseSlots = 4;
 constexpr uint32_t kTmemCols = 256;        // two score tiles of at most 128 columns
 constexpr uint32_t kRotBar = 1;            // named barrier of the rotation warps
+constexpr int kRotThreads = 256;
+constexpr int kMaxKS = 3, kMaxQG = 7;
 constexpr int kMaxSplits = 16;
 
 struct Params {
@@ -117,10 +124,25 @@ __device__ __forceinline__ void split16(float x, __half& hi, __half& lo) {
 }
 
 // ---------------------------------------------------------------- launch 1
-// Blocks 0 .. gridDim - 2: one warp per (token, 8 query heads), lane = RoPE pair.  Last block: the running
-// count of units.
+// Blocks 0 .. gridDim - 2: one warp per (token, kPrepHeads query heads), lane = RoPE pair; the rows are loaded
+// before the token's sequence is looked up.  Last block: the running count of units.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepHeads = 8;
+
+// The last entry of the ascending list at most t (n >= 1 entries, the first taken as at most t), by a warp.
+__device__ __forceinline__ int find_seq(const int32_t* list, int n, int t, int lane) {
+  int a = 0;
+  while (n > 1) {
+    const int stride = (n + 31) / 32;  // a + lane stride, the ones at most t
+    const int at = lane * stride;
+    const unsigned m = __ballot_sync(0xffffffffu, at < n && (at == 0 || __ldg(list + a + at) <= t));
+    const int k = 31 - __clz(m);
+    a += k * stride;
+    n = min(stride, n - k * stride);
+  }
+  return a;
+}
+
 __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_constant__ Params P) {
   __shared__ long long s_warp[kPrepThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -156,52 +178,58 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
   const int t = static_cast<int>(item / hblocks);
   const int h0 = static_cast<int>(item % hblocks) * kPrepHeads;
   if (t >= P.total_q) return;
-  // the token's sequence: the last one that starts at or before it
-  int a = 0, z = P.num_seqs;
-  while (z - a > 1) {
-    const int m = (a + z) / 2;
-    if (__ldg(P.cu_q + m) <= t) a = m;
-    else z = m;
-  }
+  const int nh = min(kPrepHeads, P.hq - h0);
+  const uint16_t* src = P.q + (static_cast<size_t>(t) * P.hq + h0) * kHeadDimQK;
+  uint16_t x16[kPrepHeads], y16[kPrepHeads];
+  uint2 pass[kPrepHeads];
+#pragma unroll
+  for (int i = 0; i < kPrepHeads; ++i)
+    if (i < nh) {
+      x16[i] = __ldg(src + i * kHeadDimQK + lane);
+      y16[i] = __ldg(src + i * kHeadDimQK + lane + 32);
+      pass[i] = __ldg(reinterpret_cast<const uint2*>(src + i * kHeadDimQK + 64) + lane);
+    }
+  const float l = lane < nh ? __ldg(P.lse + static_cast<size_t>(h0 + lane) * P.total_q + t) * dec::kLog2e : 0.f;
+  const double theta = P.theta[lane];
   Seq s;
-  const bool ok = load_seq(P, a, s) && t >= s.q_beg && t < s.q_beg + s.q_len;
+  const bool ok = load_seq(P, find_seq(P.cu_q, P.num_seqs, t, lane), s) && t >= s.q_beg && t < s.q_beg + s.q_len;
   if (!ok) return;  // rows of no sequence are never read as queries
-  const float2 cs = angle(s.kv_len - s.q_len + (t - s.q_beg), P.theta[lane]);
+  const float2 cs = angle(s.kv_len - s.q_len + (t - s.q_beg), theta);
   float amax = 0.f;
-#pragma unroll 4
-  for (int h = h0; h < min(h0 + kPrepHeads, P.hq); ++h) {
-    const uint16_t* src = P.q + (static_cast<size_t>(t) * P.hq + h) * kHeadDimQK;
-    const size_t row = (static_cast<size_t>(h / P.group) * P.total_q + t) * P.group + h % P.group;
-    uint16_t* dst = P.qs + row * 256;
-    const float x = __uint_as_float(static_cast<uint32_t>(__ldg(src + lane)) << 16);
-    const float y = __uint_as_float(static_cast<uint32_t>(__ldg(src + lane + 32)) << 16);
-    const float u = x * cs.x - y * cs.y, v = y * cs.x + x * cs.y;
-    amax = fmaxf(amax, fmaxf(fabsf(u), fabsf(v)));
-    __half uh, ul, vh, vl;
-    split16(u, uh, ul);
-    split16(v, vh, vl);
-    __half* d = reinterpret_cast<__half*>(dst);
-    d[lane] = uh;
-    d[lane + 32] = vh;
-    d[lane + 64] = ul;
-    d[lane + 96] = vl;
-    reinterpret_cast<uint2*>(dst + 128)[lane] = __ldg(reinterpret_cast<const uint2*>(src + 64) + lane);
-    if (lane == 0) P.lse2[row] = __ldg(P.lse + static_cast<size_t>(h) * P.total_q + t) * dec::kLog2e;
-  }
+#pragma unroll
+  for (int i = 0; i < kPrepHeads; ++i)
+    if (i < nh) {
+      const int h = h0 + i;
+      const size_t row = (static_cast<size_t>(h / P.group) * P.total_q + t) * P.group + h % P.group;
+      uint16_t* dst = P.qs + row * 256;
+      const float x = __uint_as_float(static_cast<uint32_t>(x16[i]) << 16);
+      const float y = __uint_as_float(static_cast<uint32_t>(y16[i]) << 16);
+      const float u = x * cs.x - y * cs.y, v = y * cs.x + x * cs.y;
+      amax = fmaxf(amax, fmaxf(fabsf(u), fabsf(v)));
+      __half uh, ul, vh, vl;
+      split16(u, uh, ul);
+      split16(v, vh, vl);
+      __half* d = reinterpret_cast<__half*>(dst);
+      d[lane] = uh;
+      d[lane + 32] = vh;
+      d[lane + 64] = ul;
+      d[lane + 96] = vl;
+      reinterpret_cast<uint2*>(dst + 128)[lane] = pass[i];
+      if (lane == i) P.lse2[row] = l;
+    }
   if (amax > 65504.f) atomicOr(&g_mimo_error, kErrRange);
 }
 
 // ---------------------------------------------------------------- launch 2
 struct Ctrl {
-  uint64_t k_landed[2], k_full[2], k_empty[2];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t k_landed[kMaxKS], k_full[kMaxKS], k_empty[kMaxKS], lo_empty;
+  uint64_t q_full[kMaxQG], q_empty[kMaxQG];
   uint64_t s_full[2], s_empty[2];
   uint64_t lse_full[kLseSlots];
   uint32_t tmem_base;
   int abort;
-  float2 k_base[2][kRopeDims / 2];  // cos / sin at the tile's first key, by unit parity
-  double theta[kRopeDims / 2];
-  float lse2[kLseSlots][kTile];     // of the Q loads, in turn
+  alignas(16) float k_cos[2][kRopeDims / 2], k_sin[2][kRopeDims / 2];  // at the tile's first key, by tile parity
+  alignas(16) float lse2[kLseSlots][kTile];                // of the Q loads, in turn (read as float4)
 };
 constexpr uint32_t kSmemBytes = kCtrlOff + ((sizeof(Ctrl) + 15) & ~size_t(15));
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -220,6 +248,7 @@ struct Walker {
   long long u, step, left;
   int b = -1;
   long long lo = 0, hi = 0;  // units of sequence b
+  int kt = 0, f = 0, g = 0, nq = 0;
   Seq s;
   __device__ __forceinline__ explicit Walker(const Params& P) {
     const long long total = P.units[P.num_seqs];
@@ -244,32 +273,47 @@ struct Walker {
   }
   __device__ __forceinline__ bool next(const Params& P, Unit& w) {
     if (left == 0) return false;
+    bool place = step > 1 || u >= hi;  // else: the unit after the last one, in the same sequence
     while (u >= hi) {
       ++b;
       lo = P.units[b];
       hi = P.units[b + 1];
       load_seq(P, b, s);
+      nq = (s.q_len * P.group + P.ntile - 1) / P.ntile;
     }
-    const int r = static_cast<int>(u - lo);
-    const int kt = r % s.tiles, r2 = r / s.tiles;
-    w.f = r2 % P.splits;
-    w.g = r2 / P.splits;
+    if (place) {
+      const int r = static_cast<int>(u - lo), r2 = r / s.tiles;
+      kt = r - r2 * s.tiles;
+      g = r2 / P.splits;
+      f = r2 - g * P.splits;
+    } else if (++kt == s.tiles) {
+      kt = 0;
+      if (++f == P.splits) {
+        f = 0;
+        ++g;
+      }
+    }
+    w.f = f;
+    w.g = g;
     w.kv_beg = s.kv_beg;
     w.kv_len = s.kv_len;
     w.k0 = s.lo + kt * kTile;
     w.nk = min(kTile, s.kv_len - w.k0);
     w.p0 = s.kv_len - s.q_len;
     w.rows = s.q_len * P.group;
-    const int nq = (w.rows + P.ntile - 1) / P.ntile;
-    w.qt0 = static_cast<int>(static_cast<long long>(nq) * w.f / P.splits);
-    w.qt1 = static_cast<int>(static_cast<long long>(nq) * (w.f + 1) / P.splits);
-    if (w.k0 > w.p0)  // causal: rows from the query at the tile's first key on
-      w.qt0 = max(w.qt0, static_cast<int>(static_cast<long long>(w.k0 - w.p0) * P.group / P.ntile));
-    if (P.window >= 0) {  // rows up to the last query whose window reaches the tile's last key
-      const long long end = (static_cast<long long>(w.k0) + w.nk + P.window - w.p0) * P.group;
-      w.qt1 = static_cast<int>(min(static_cast<long long>(w.qt1), (end + P.ntile - 1) / P.ntile));
+    w.qt0 = 0;
+    w.qt1 = nq;
+    if (!P.contiguous) {
+      w.qt0 = static_cast<int>(static_cast<long long>(nq) * f / P.splits);
+      w.qt1 = static_cast<int>(static_cast<long long>(nq) * (f + 1) / P.splits);
+      if (w.k0 > w.p0)  // causal: rows from the query at the tile's first key on
+        w.qt0 = max(w.qt0, static_cast<int>(static_cast<long long>(w.k0 - w.p0) * P.group / P.ntile));
+      if (P.window >= 0) {  // rows up to the last query whose window reaches the tile's last key
+        const long long end = (static_cast<long long>(w.k0) + w.nk + P.window - w.p0) * P.group;
+        w.qt1 = static_cast<int>(min(static_cast<long long>(w.qt1), (end + P.ntile - 1) / P.ntile));
+      }
     }
-    w.row0 = (static_cast<long long>(w.g) * P.total_q + s.q_beg) * P.group;
+    w.row0 = (static_cast<long long>(g) * P.total_q + s.q_beg) * P.group;
     u += step;
     --left;
     return true;
@@ -318,7 +362,7 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   for (uint32_t c = 0; more; ++c) {
     const uint32_t st = c % KS;
     if (c >= KS && !wait(C, &C->k_empty[st], (c / KS - 1) & 1, P.wait_limit_ns)) break;
-    const uint32_t dst = smem_u32(smem + st * kStage);
+    const uint32_t dst = smem_u32(smem + kRingOff + st * kStage);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int j = 16 * p + rsub;
@@ -338,52 +382,64 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   if (bad) atomicOr(&g_mimo_error, kErrSeqlens);
 }
 
+// Thread: key r = t % 128 of the tile, chunk pairs 2h and 2h + 1 (dims 16h .. 16h + 15 and their partners),
+// h = t / 128.
 template <int KS>
-__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params& P, int r) {
-  // cos / sin of this row's offset from the tile's first key
-  float2 off[kRopeDims / 2];
+__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params& P, int t) {
+  const int r = t & 127, h = t >> 7;
+  // cos / sin of this key's offset from the tile's first key, two frequencies to a pair
+  float2 oc[8], os[8];
 #pragma unroll
-  for (int i = 0; i < kRopeDims / 2; ++i) off[i] = angle(r, C->theta[i]);
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = angle(r, P.theta[16 * h + 2 * i]), b = angle(r, P.theta[16 * h + 2 * i + 1]);
+    oc[i] = make_float2(a.x, b.x);
+    os[i] = make_float2(a.y, b.y);
+  }
+  const double theta = t < kRopeDims / 2 ? P.theta[t] : 0.0;
   Walker walk(P);
   Unit w;
-  float amax = 0.f;
+  __half2 amax = __floats2half2_rn(0.f, 0.f);
   bool ok = true;
 #pragma unroll 1
   for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
     const uint32_t st = c % KS;
-    if (r < kRopeDims / 2) C->k_base[c & 1][r] = angle(w.k0, C->theta[r]);
+    if (t < kRopeDims / 2) {
+      const float2 a = angle(w.k0, theta);
+      C->k_cos[c & 1][t] = a.x;
+      C->k_sin[c & 1][t] = a.y;
+    }
     if (ok) ok = wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
+    if (ok && c > 0) ok = wait(C, &C->lo_empty, (c - 1) & 1, P.wait_limit_ns);
     // this tile's base angles written, those of two tiles back read; all leave together
-    if (!named_bar_and(kRotBar, 128, ok)) break;
-    const float2* base = C->k_base[c & 1];
-    uint8_t* hi_row = smem + st * kStage + r * 128;
-    uint8_t* lo_row = hi_row + 3 * kUnit;
+    if (!named_bar_and(kRotBar, kRotThreads, ok)) break;
+    uint8_t* hi_row = smem + kRingOff + st * kStage + r * 128;
+    uint8_t* lo_row = smem + kLoOff + r * 128;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {  // chunk pair (p, p + 4): dims 8p .. 8p + 7 and their partners
+    for (int q = 0; q < 2; ++q) {
+      const int p = 2 * h + q;
       const uint32_t ca = (p ^ (r & 7)) << 4, cb = ((p + 4) ^ (r & 7)) << 4;
       const uint4 a = *reinterpret_cast<const uint4*>(hi_row + ca), b = *reinterpret_cast<const uint4*>(hi_row + cb);
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
       uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float u[2], v[2];
+        const float2 bc = *reinterpret_cast<const float2*>(&C->k_cos[c & 1][8 * p + 2 * e]);
+        const float2 bs = *reinterpret_cast<const float2*>(&C->k_sin[c & 1][8 * p + 2 * e]);
+        const float2 kc = oc[4 * q + e], ks = os[4 * q + e];
+        const float2 cs = ffma2(bc, kc, fmul2(make_float2(-bs.x, -bs.y), ks));
+        const float2 sn = ffma2(bs, kc, fmul2(bc, ks));
         const float2 x = unpack_bf16x2(aw[e]), y = unpack_bf16x2(bw[e]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 t = base[8 * p + 2 * e + k], o = off[8 * p + 2 * e + k];
-          const float cs = t.x * o.x - t.y * o.y, sn = t.y * o.x + t.x * o.y;
-          const float xx = k ? x.y : x.x, yy = k ? y.y : y.x;
-          u[k] = xx * cs - yy * sn;
-          v[k] = yy * cs + xx * sn;
-          amax = fmaxf(amax, fmaxf(fabsf(u[k]), fabsf(v[k])));
-        }
-        const __half2 uh = __floats2half2_rn(u[0], u[1]), vh = __floats2half2_rn(v[0], v[1]);
-        const float2 uf = __half22float2(uh), vf = __half22float2(vh);
-        const __half2 ul = __floats2half2_rn(u[0] - uf.x, u[1] - uf.y), vl = __floats2half2_rn(v[0] - vf.x, v[1] - vf.y);
+        const float2 ny = unpack_bf16x2(bw[e] ^ 0x80008000u);
+        const float2 u = ffma2(x, cs, fmul2(ny, sn)), v = ffma2(y, cs, fmul2(x, sn));
+        const __half2 uh = __floats2half2_rn(u.x, u.y), vh = __floats2half2_rn(v.x, v.y);
+        amax = __hmax2(amax, __hmax2(__habs2(uh), __habs2(vh)));
+        const float2 m1 = make_float2(-1.f, -1.f);
+        const float2 ul = ffma2(__half22float2(uh), m1, u), vl = ffma2(__half22float2(vh), m1, v);
+        const __half2 uln = __floats2half2_rn(ul.x, ul.y), vln = __floats2half2_rn(vl.x, vl.y);
         ah[e] = *reinterpret_cast<const uint32_t*>(&uh);
-        al[e] = *reinterpret_cast<const uint32_t*>(&ul);
+        al[e] = *reinterpret_cast<const uint32_t*>(&uln);
         bh[e] = *reinterpret_cast<const uint32_t*>(&vh);
-        bl[e] = *reinterpret_cast<const uint32_t*>(&vl);
+        bl[e] = *reinterpret_cast<const uint32_t*>(&vln);
       }
       *reinterpret_cast<uint4*>(hi_row + ca) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
       *reinterpret_cast<uint4*>(hi_row + cb) = make_uint4(bh[0], bh[1], bh[2], bh[3]);
@@ -393,86 +449,124 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params
     fence_proxy_async_smem();  // the fetcher's copies and these writes, before the MMA reads the stage
     mbar_arrive(&C->k_full[st]);
   }
-  if (amax > 65504.f) atomicOr(&g_mimo_error, kErrRange);
+  const float2 top = __half22float2(amax);
+  if (fmaxf(top.x, top.y) > 65504.f) atomicOr(&g_mimo_error, kErrRange);  // infinite: rounded past FP16's range
 }
 
-template <int QS>
+template <int KS, int QG>
 __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params& P, const CUtensorMap* tq, int lane) {
+  uint8_t* ring = smem + kRingOff + KS * kStage;
   Walker walk(P);
   Unit w;
   long long have = -1;
-  uint32_t loads = 0;
-  const uint32_t unit_bytes = static_cast<uint32_t>(P.ntile) * 128u;
+  uint32_t loads = 0, gi = 0;  // Q tiles, granules
+  const uint32_t bytes = static_cast<uint32_t>(P.ntile) * 128u;
   bool ok = true;
 #pragma unroll 1
   while (ok && walk.next_busy(P, w)) {
 #pragma unroll 1
-    for (int qt = w.qt0; qt < w.qt1; ++qt) {
+    for (int qt = w.qt0; ok && qt < w.qt1; ++qt) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
-      if (row == have) continue;
+      if (QG == 4 && row == have) continue;  // with more granules each use hands them back
       have = row;
-      const uint32_t st = loads % QS;
-      ok = loads < QS || wait(C, &C->q_empty[st], (loads / QS - 1) & 1, P.wait_limit_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      for (int c = lane; c < P.ntile; c += 32)
-        C->lse2[loads % kLseSlots][c] = qt * P.ntile + c < w.rows ? __ldg(P.lse2 + row + c) : 0.f;
-      uint8_t* dst = smem + (3 - QS + st) * kStage;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&C->q_full[st], 4 * unit_bytes);
-        for (int u = 0; u < 4; ++u)
-          tma_load_2d(dst + u * kUnit, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u, ++gi) {
+        const uint32_t st = gi % QG;
+        ok = gi < QG || wait(C, &C->q_empty[st], (gi / QG - 1) & 1, P.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&C->q_full[st], bytes);
+          tma_load_2d(ring + st * kUnit, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
+        }
+        if (u == 0) {
+          // the products that this granule waited for are two tiles back at most, and the sums two behind
+          // those, so the slot's last reader is done
+          for (int c = lane; c < P.ntile; c += 32)
+            C->lse2[loads % kLseSlots][c] = qt * P.ntile + c < w.rows ? __ldg(P.lse2 + row + c) : 0.f;
+          mbar_arrive(&C->lse_full[loads % kLseSlots]);
+        }
       }
-      mbar_arrive(&C->lse_full[loads % kLseSlots]);
-      ++loads;
+      if (ok) ++loads;
     }
   }
   // nothing of ours stays in flight, on every path
-  if (loads > 0) wait(C, &C->q_full[(loads - 1) % QS], ((loads - 1) / QS) & 1, P.wait_limit_ns);
-  if (QS > 1 && loads > 1) wait(C, &C->q_full[(loads - 2) % QS], ((loads - 2) / QS) & 1, P.wait_limit_ns);
+  for (uint32_t i = gi > QG ? gi - QG : 0; i < gi; ++i) wait(C, &C->q_full[i % QG], (i / QG) & 1, P.wait_limit_ns);
 }
 
-template <int KS, int QS>
+template <int KS, int QG>
 __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P) {
   const uint32_t idesc_f16 = make_idesc_f32acc(0, 0, 128, P.ntile), idesc_bf16 = make_idesc_f32acc(1, 0, 128, P.ntile);
   constexpr uint32_t kStep = kUnit >> 4;
+  const uint32_t lo = sdesc_lo(smem_u32(smem + kLoOff), 16);
+  const uint32_t ring = smem_u32(smem + kRingOff + KS * kStage);
   Walker walk(P);
   Unit w;
   long long have = -1;
-  uint32_t loads = 0, d = 0;
+  uint32_t gi = 0, d = 0;  // granules of the Q tiles before the current one; score tiles
+  bool any = false;
 #pragma unroll 1
   for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
     const uint32_t st = c % KS;
     if (!wait(C, &C->k_full[st], (c / KS) & 1, P.wait_limit_ns)) return;
-    const uint32_t k_lo = sdesc_lo(smem_u32(smem + st * kStage), 16);
+    const uint32_t hi = sdesc_lo(smem_u32(smem + kRingOff + st * kStage), 16);
 #pragma unroll 1
     for (int qt = w.qt0; qt < w.qt1; ++qt, ++d) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
-      if (row != have) {
-        if (loads > 0) tc_commit(&C->q_empty[(loads - 1) % QS]);  // the last product with those rows is issued
-        have = row;
-        if (!wait(C, &C->q_full[loads % QS], (loads / QS) & 1, P.wait_limit_ns)) return;
-        ++loads;
+      const bool fresh = QG > 4 || row != have;
+      if (fresh && any) {  // the last product with the rows before is issued: hand them back
+        if (QG == 4)
+          for (int u = 0; u < 4; ++u) tc_commit(&C->q_empty[u]);
+        gi += 4;
       }
+      have = row;
+      any = true;
+      const bool last = qt + 1 == w.qt1;
       if (d >= 2 && !wait(C, &C->s_empty[d & 1], ((d >> 1) - 1) & 1, P.wait_limit_ns)) return;
-      tc_fence_after_sync();
-      const uint32_t q_lo = sdesc_lo(smem_u32(smem + (3 - QS + (loads - 1) % QS) * kStage), 16);
       const uint32_t acc = tmem + 128u * (d & 1);
-      // rotated dims: hi hi, hi lo, lo hi; then the pass-through dims
+      // granule u of the tile: Q hi with K lo and K hi, Q lo with K hi, then the pass-through dims
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_ss_lo(acc, k_lo + 2 * k, q_lo + 2 * k, idesc_f16, k > 0 ? 1u : 0u);
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t slot = (gi + u) % QG;
+        if (fresh && !wait(C, &C->q_full[slot], ((gi + u) / QG) & 1, P.wait_limit_ns)) return;
+        if (u == 0 || fresh) tc_fence_after_sync();
+        const uint32_t q = sdesc_lo(ring + slot * kUnit, 16);
+        if (u == 0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_ss_lo(acc, k_lo + 2 * k, q_lo + kStep + 2 * k, idesc_f16, 1u);
+          for (int k = 0; k < 4; ++k) mma_ss_lo(acc, lo + 2 * k, q + 2 * k, idesc_f16, k > 0 ? 1u : 0u);
+          if (last) tc_commit(&C->lo_empty);
+        }
+        const uint32_t a = hi + (u < 2 ? 0u : (u - 1) * kStep);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_ss_lo(acc, k_lo + 3 * kStep + 2 * k, q_lo + 2 * k, idesc_f16, 1u);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss_lo(acc, k_lo + (1 + u) * kStep + 2 * k, q_lo + (2 + u) * kStep + 2 * k, idesc_bf16, 1u);
+        for (int k = 0; k < 4; ++k) mma_ss_lo(acc, a + 2 * k, q + 2 * k, u < 2 ? idesc_f16 : idesc_bf16, 1u);
+        if (QG > 4) tc_commit(&C->q_empty[slot]);
+      }
       tc_commit(&C->s_full[d & 1]);
     }
     tc_commit(&C->k_empty[st]);
+  }
+}
+
+// Adds 2^(s sl2 - lse2) over N score columns; masked: of those in [lo, hi) only.
+template <int N, bool kMasked>
+__device__ __forceinline__ void add_columns(const uint32_t (&s)[N], const float* lse2, float sl2, int lo, int hi,
+                                            float2& a0, float2& a1) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(lse2 + i);
+    const float2 k = make_float2(sl2, sl2);
+    const float2 e0 = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k, make_float2(-l.x, -l.y));
+    const float2 e1 =
+        ffma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), k, make_float2(-l.z, -l.w));
+    float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y)), p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+    if (kMasked) {
+      p0.x = i >= lo && i < hi ? p0.x : 0.f;
+      p0.y = i + 1 >= lo && i + 1 < hi ? p0.y : 0.f;
+      p1.x = i + 2 >= lo && i + 2 < hi ? p1.x : 0.f;
+      p1.y = i + 3 >= lo && i + 3 < hi ? p1.y : 0.f;
+    }
+    a0 = fadd2(a0, p0);
+    a1 = fadd2(a1, p1);
   }
 }
 
@@ -486,51 +580,64 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
 #pragma unroll 1
   while (walk.next(P, w)) {
     const int key = w.k0 + r;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll 1
     for (int qt = w.qt0; qt < w.qt1; ++qt, ++d) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
       bool ok = true;
-      if (row != have) {
-        // this load's lse; the loader is at most three loads ahead (its rows wait for the products of the
-        // load before, and those for the score tiles), so the slot still holds it
+      if (row != have || !P.contiguous) {
+        // this load's lse; the loader is at most two loads ahead (its rows wait for the products of the
+        // loads before, and those for the score tiles), so the slot still holds it
         have = row;
         ok = wait(C, &C->lse_full[loads % kLseSlots], (loads / kLseSlots) & 1, P.wait_limit_ns);
         ++loads;
       }
       const float* lse2 = C->lse2[(loads - 1) % kLseSlots];
-      // columns (query rows) that see this key: a run
-      const long long base = static_cast<long long>(qt) * P.ntile;
-      const long long seen = (static_cast<long long>(key) - w.p0) * P.group - base;
-      const int c_lo = static_cast<int>(max(0LL, min(seen, 128LL)));
-      long long c_end = min(static_cast<long long>(P.ntile), w.rows - base);
-      if (P.window >= 0) c_end = min(c_end, (static_cast<long long>(key) + P.window + 1 - w.p0) * P.group - base);
-      const int c_hi = static_cast<int>(max(0LL, c_end));
+      const int base = qt * P.ntile, cols = min(P.ntile, w.rows - base);  // query rows of the tile
+      // the tile's first query sees the unit's last key, and the last one's window holds its first key
+      const bool all = w.p0 + base / P.group >= w.k0 + w.nk - 1 &&
+                       (P.window < 0 || w.k0 + P.window >= w.p0 + (base + cols - 1) / P.group);
+      int c_lo = 0, c_hi = cols;
+      if (!all) {  // columns (query rows) that see this key: a run
+        const long long seen = (static_cast<long long>(key) - w.p0) * P.group - base;
+        c_lo = static_cast<int>(max(0LL, min(seen, 128LL)));
+        if (P.window >= 0) {
+          const long long end = (static_cast<long long>(key) + P.window + 1 - w.p0) * P.group - base;
+          c_hi = static_cast<int>(max(0LL, min(static_cast<long long>(cols), end)));
+        }
+      }
       if (!__all_sync(0xffffffffu, ok && wait(C, &C->s_full[d & 1], (d >> 1) & 1, P.wait_limit_ns))) return;
       tc_fence_after_sync();
+      const uint32_t acc = tmem + lane_base + 128u * (d & 1);
+      int c0 = 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < P.ntile; c0 += 16) {
+      for (; c0 + 32 <= cols; c0 += 32) {
+        uint32_t s[32];
+        tmem_ld32(acc + c0, s);
+        tmem_ld_wait(s);
+        if (all) add_columns<32, false>(s, lse2 + c0, sl2, 0, 0, a0, a1);
+        else add_columns<32, true>(s, lse2 + c0, sl2, c_lo - c0, c_hi - c0, a0, a1);
+      }
+#pragma unroll 1
+      for (; c0 < cols; c0 += 16) {  // ntile is a multiple of 16
         uint32_t s[16];
-        tmem_ld16(tmem + lane_base + 128u * (d & 1) + c0, s);
+        tmem_ld16(acc + c0, s);
         tmem_ld16_wait(s);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p = ex2_approx(fmaf(__uint_as_float(s[i]), sl2, -lse2[c0 + i]));
-          acc[i & 3] += (c0 + i >= c_lo && c0 + i < c_hi) ? p : 0.f;
-        }
+        if (all && c0 + 16 <= cols) add_columns<16, false>(s, lse2 + c0, sl2, 0, 0, a0, a1);
+        else add_columns<16, true>(s, lse2 + c0, sl2, c_lo - c0, c_hi - c0, a0, a1);
       }
       tc_fence_before_sync();
       mbar_arrive(&C->s_empty[d & 1]);
     }
     if (r < w.nk)
-      P.partial[(static_cast<size_t>(w.f) * P.hkv + w.g) * P.total_kv + w.kv_beg + key] =
-          (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      P.partial[(static_cast<size_t>(w.f) * P.hkv + w.g) * P.total_kv + w.kv_beg + key] = (a0.x + a0.y) + (a1.x + a1.y);
   }
 }
 
-template <int KS, int QS>
+template <int KS, int QG>
 __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_constant__ CUtensorMap tq,
                                                               const __grid_constant__ Params P) {
+  static_assert(KS <= kMaxKS && QG <= kMaxQG && kRingOff + KS * kStage + QG * kUnit <= kCtrlOff, "rings");
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctrl* C = reinterpret_cast<Ctrl*>(smem + kCtrlOff);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -541,12 +648,17 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
   }
   if (__syncthreads_or(skip)) return;
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < KS; ++s) {
       mbar_init(&C->k_landed[s], 128);  // one cp.async arrival per fetcher thread
-      mbar_init(&C->k_full[s], 128);
+      mbar_init(&C->k_full[s], kRotThreads);
       mbar_init(&C->k_empty[s], 1);
+    }
+    mbar_init(&C->lo_empty, 1);
+    for (int s = 0; s < QG; ++s) {
       mbar_init(&C->q_full[s], 1);
       mbar_init(&C->q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&C->s_full[s], 1);
       mbar_init(&C->s_empty[s], 128);
     }
@@ -554,8 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     C->abort = 0;
     fence_barrier_init();
   }
-  if (tid < kRopeDims / 2) C->theta[tid] = P.theta[tid];
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(&C->tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -567,17 +678,17 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     role_sum(C, tmem, P, tid, warp);
   } else if (warp < 8) {
     role_fetch<KS>(smem, C, P, tid - 128);
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     role_rotate<KS>(smem, C, P, tid - 256);
-  } else if (warp == 12) {
-    if ((tid & 31) == 0) role_mma<KS, QS>(smem, C, tmem, P);
+  } else if (warp == 16) {
+    if ((tid & 31) == 0) role_mma<KS, QG>(smem, C, tmem, P);
   } else {
-    role_load_q<QS>(smem, C, P, &tq, tid & 31);
+    role_load_q<KS, QG>(smem, C, P, &tq, tid & 31);
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -587,19 +698,26 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) kw_join_kernel(const __grid_constant__ Params P) {
   const long long i = static_cast<long long>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  if (i >= P.total_kv) return;
-  int a = 0, z = P.num_seqs;
-  while (z - a > 1) {
-    const int m = (a + z) / 2;
-    if (__ldg(P.kv_indptr + m) <= i) a = m;
-    else z = m;
-  }
-  Seq s;
-  if (!load_seq(P, a, s) || i < s.kv_beg || i >= s.kv_beg + s.kv_len) return;  // left as it was
+  const int lane = threadIdx.x & 31;
+  const bool in = i < P.total_kv;
+  const int rows = P.splits * P.hkv;
+  // the partial rows are read before the entry's sequence is known: where no query sees the key they were not
+  // written, and what is read does not count
   float v = 0.f;
-  if (i - s.kv_beg >= s.lo)
-    for (int k = 0; k < P.splits * P.hkv; ++k) v += P.partial[static_cast<size_t>(k) * P.total_kv + i];
-  P.out[i] = P.prev != nullptr ? P.prev[i] + v : v;
+  if (in) {
+#pragma unroll 4
+    for (int k = 0; k < rows; ++k) v += P.partial[static_cast<size_t>(k) * P.total_kv + i];
+  }
+  const float p = in && P.prev != nullptr ? P.prev[i] : 0.f;
+  // the sequence of the warp's first entry, and from there on to this entry's
+  const long long i0 = i - lane;
+  if (i0 >= P.total_kv) return;
+  int b = find_seq(P.kv_indptr, P.num_seqs, static_cast<int>(i0), lane);
+  if (!in) return;
+  while (b + 1 < P.num_seqs && __ldg(P.kv_indptr + b + 1) <= i) ++b;
+  Seq s;
+  if (!load_seq(P, b, s) || i < s.kv_beg || i >= s.kv_beg + s.kv_len) return;  // left as it was
+  P.out[i] = i - s.kv_beg >= s.lo ? p + v : p;
 }
 
 }  // namespace kw

@@ -195,9 +195,9 @@ bool key_weights_ready(int dev) {
   static std::atomic<int> state[64];  // 0 unknown, 1 ready, -1 failed
   if (dev < 0 || dev >= 64) return false;
   if (state[dev].load() == 0)
-    state[dev].store(cudaFuncSetAttribute(kw::kw_main_kernel<2, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    state[dev].store(cudaFuncSetAttribute(kw::kw_main_kernel<3, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           kw::kSmemBytes) == cudaSuccess &&
-                             cudaFuncSetAttribute(kw::kw_main_kernel<1, 2>,
+                             cudaFuncSetAttribute(kw::kw_main_kernel<2, 7>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   kw::kSmemBytes) == cudaSuccess
                          ? 1
@@ -915,9 +915,9 @@ int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const 
     const long long units = ((long long)d->total_kv / kw::kTile + d->num_seqs) * P.hkv * P.splits;
     const unsigned grid = (unsigned)std::min<long long>(units, info->sms);
     if (P.contiguous)
-      kw::kw_main_kernel<2, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+      kw::kw_main_kernel<3, 4><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     else
-      kw::kw_main_kernel<1, 2><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+      kw::kw_main_kernel<2, 7><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     if (cudaGetLastError() != cudaSuccess) return MIMO_ERR_CUDA;
   }
   kw::kw_join_kernel<<<(unsigned)(((long long)d->total_kv + kw::kJoinThreads - 1) / kw::kJoinThreads),

@@ -77,8 +77,9 @@ def adapt_pair_kernel(s):
     return s
 
 
-def build(out_dir: str, src_root: str = ROOT, mutations=()) -> str:
-    """mutations: (file, old text, new text) applied to the copied sources (planted-mistake tests)."""
+def build(out_dir: str, src_root: str = ROOT, mutations=(), flags=()) -> str:
+    """mutations: (file, old text, new text) applied to the copied sources (planted-mistake tests); flags: further
+    compiler flags."""
     # the repository's layout, so that the API file finds its header by its relative path
     csrc = os.path.join(out_dir, "global_attention_moe_b200", "csrc")
     shutil.rmtree(os.path.join(out_dir, "global_attention_moe_b200"), ignore_errors=True)
@@ -122,7 +123,7 @@ def build(out_dir: str, src_root: str = ROOT, mutations=()) -> str:
                 f'#include "{os.path.join(csrc, "mimo_attn_api.cu")}"\n'
                 '#include "tensormap_host.h"\n' + EXPORTS)
     so = os.path.join(out_dir, "libmimo_attn_host.so")
-    cmd = ["g++", "-std=c++20", "-O2", "-fno-strict-aliasing", "-fPIC", "-shared", "-w", "-Wl,-Bsymbolic",
+    cmd = ["g++", *flags, "-std=c++20", "-O2", "-fno-strict-aliasing", "-fPIC", "-shared", "-w", "-Wl,-Bsymbolic",
            "-I/usr/local/cuda/include", "-I" + HERE, tu, "-o", so]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:

@@ -559,4 +559,6 @@ inline float rcp_approx(float x) {
   return std::fabs(y) < 1.17549435e-38f ? std::copysign(0.f, y) : y;
 }
 
+inline float2 fmul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+
 }  // namespace mimo

@@ -423,6 +423,7 @@ inline int __reduce_max_sync(unsigned, int v) { return hemu_reduce(v, [](int a, 
 inline int __reduce_min_sync(unsigned, int v) { return hemu_reduce(v, [](int a, int b) { return a < b ? a : b; }); }
 inline int __reduce_add_sync(unsigned, int v) { return hemu_reduce(v, [](int a, int b) { return a + b; }); }
 inline int __popc(unsigned v) { return __builtin_popcount(v); }
+inline int __clz(unsigned v) { return v ? __builtin_clz(v) : 32; }
 inline int __ffs(unsigned v) { return __builtin_ffs(static_cast<int>(v)); }
 inline float __fdiv_rn(float a, float b) { return a / b; }
 inline float __fmul_rn(float a, float b) { return a * b; }  // SSE: one IEEE rounding, subnormals kept

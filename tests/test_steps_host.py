@@ -18,7 +18,17 @@ from oracle import steps  # noqa: E402
 
 @pytest.fixture(scope="module")
 def host_library(tmp_path_factory):
-    return build_library.build(str(tmp_path_factory.mktemp("steps_host")))
+    # a vector load or store off its alignment, which the GPU faults on, ends the case
+    return build_library.build(str(tmp_path_factory.mktemp("steps_host")),
+                               flags=("-fsanitize=alignment", "-fno-sanitize-recover=alignment"))
+
+
+def test_alignment_is_checked(tmp_path):
+    """Planted: the lse slots of the key-weights kernel 8 bytes off (float4 reads need 16)."""
+    lib = build_library.build(str(tmp_path), flags=("-fsanitize=alignment", "-fno-sanitize-recover=alignment"), mutations=[
+        ("key_weights.cuh", "alignas(16) float k_cos", "float k_cos"), ("key_weights.cuh", "alignas(16) float lse2", "float lse2")])
+    rc, log = run(lib, ["weights_step"])
+    assert rc != 0 and "alignment" in log, log
 
 
 def run(lib, names, sms=None):
