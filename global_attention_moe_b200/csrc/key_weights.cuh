@@ -27,16 +27,18 @@
 // Warp roles of the main kernel (18 warps):
 //   warps 0-3   sums (thread = key = TMEM lane)
 //   warps 4-7   K fetcher: gathers the tile's rows by index with cp.async into the 128-byte-swizzled layout
-//   warps 8-15  K rotation, two threads to a key: BF16 -> FP16 hi in place, lo into a buffer of its own
-//               (angle addition from the tile's first key; paired FP32 arithmetic)
-//   warp 16     TMEM owner; lane 0 issues the MMAs
+//   warps 8-15  K rotation, two threads to a key: rows from shared memory, BF16 -> FP16 hi and lo (angle
+//               addition from the tile's first key; paired FP32 arithmetic), into TMEM with the pass dims
+//   warp 16     TMEM owner; lane 0 issues the MMAs (A = K from TMEM, B = Q from shared memory)
 //   warp 17     Q loader: TMA boxes of the prepared rows, and their lse
-// Units are walked in order by every role.  K tiles go through a ring of KS stages (48 KB: hi, pass, pass), Q
-// tiles through a ring of QG granules of 128 rows x 64 dims (hi, lo, pass, pass of each tile in turn), each
-// handed back as soon as its products are done.  With one query tile per sequence (decode steps) a CTA takes a
-// contiguous run of units, so Q stays in its four granules while the keys of a (sequence, KV head) stream
-// through three stages; with more (chunked prefill) a key tile stays in one of two stages while the query
-// tiles stream through seven granules.
+// Units are walked in order by every role.  A gathered K tile (48 KB) stays in its stage only until it has been
+// rotated into one of two TMEM buffers (128 columns: hi, lo, pass): the gather's latency, about 2.5 us for rows
+// spread over the cache, is what has to be covered, and the stages are what covers it.  It also leaves the
+// tensor cores one operand to read from shared memory instead of two, whose 128 bytes a cycle they would
+// take whole.  Q tiles go through granules of ntile rows x 64 dims (hi, lo, pass, pass).  With one query tile
+// per sequence (decode steps) a CTA takes a contiguous run of units, so Q stays in its four granules while
+// the keys of a (sequence, KV head) stream through KS stages; with more (chunked prefill) a key tile stays in
+// TMEM while the query tiles stream through two sets of granules.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -48,15 +50,14 @@ namespace kw {
 constexpr int kThreads = 576;
 constexpr int kTile = 128;             // keys per unit
 constexpr uint32_t kUnit = 16384;      // 128 rows x 64 dims x 2 B
-constexpr uint32_t kStage = 3 * kUnit;  // K: hi, pass, pass
-constexpr uint32_t kLoOff = 0;         // the rotated dims' low parts of one K tile
-constexpr uint32_t kRingOff = kUnit;   // KS stages, then QG granules: 13 units
-constexpr uint32_t kCtrlOff = 14 * kUnit;
+constexpr uint32_t kStage = 3 * kUnit;  // a gathered K tile: dims 0..63, 64..127, 128..191
+constexpr uint32_t kCtrlOff = 14 * kUnit;  // KS stages, then QG granules
 constexpr int kLseSlots = 4;
-constexpr uint32_t kTmemCols = 256;        // two score tiles of at most 128 columns
+constexpr uint32_t kTmemCols = 512;        // two score tiles of at most 128 columns, then two K tiles
+constexpr uint32_t kColK = 256;
 constexpr uint32_t kRotBar = 1;            // named barrier of the rotation warps
 constexpr int kRotThreads = 256;
-constexpr int kMaxKS = 3, kMaxQG = 7;
+constexpr int kMaxKS = 4, kMaxQG = 8;
 constexpr int kMaxSplits = 16;
 
 struct Params {
@@ -108,8 +109,8 @@ __device__ __forceinline__ bool load_seq(const Params& P, int b, Seq& s) {
   return true;
 }
 
-// cos / sin of pos theta, the angle reduced in FP64.
-__device__ __forceinline__ float2 angle(int pos, double theta) {
+// cos / sin of pos theta, the angle reduced in FP64 (out of line: every copy of sincosf is a few KB of code).
+__device__ __noinline__ float2 angle(int pos, double theta) {
   const double a = static_cast<double>(pos) * theta;
   const double n = rint(a * kInvTwoPi);
   float s, c;
@@ -222,7 +223,8 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
 
 // ---------------------------------------------------------------- launch 2
 struct Ctrl {
-  uint64_t k_landed[kMaxKS], k_full[kMaxKS], k_empty[kMaxKS], lo_empty;
+  uint64_t k_landed[kMaxKS], k_empty[kMaxKS];  // stages
+  uint64_t k_full[2], k_free[2];               // K tiles in TMEM
   uint64_t q_full[kMaxQG], q_empty[kMaxQG];
   uint64_t s_full[2], s_empty[2];
   uint64_t lse_full[kLseSlots];
@@ -362,7 +364,7 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   for (uint32_t c = 0; more; ++c) {
     const uint32_t st = c % KS;
     if (c >= KS && !wait(C, &C->k_empty[st], (c / KS - 1) & 1, P.wait_limit_ns)) break;
-    const uint32_t dst = smem_u32(smem + kRingOff + st * kStage);
+    const uint32_t dst = smem_u32(smem + st * kStage);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int j = 16 * p + rsub;
@@ -382,11 +384,12 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   if (bad) atomicOr(&g_mimo_error, kErrSeqlens);
 }
 
-// Thread: key r = t % 128 of the tile, chunk pairs 2h and 2h + 1 (dims 16h .. 16h + 15 and their partners),
-// h = t / 128.
+// Thread: key r = t % 128 of the tile (the TMEM lane), h = t / 128: chunk pairs 2h and 2h + 1 (dims 16h ..
+// 16h + 15 and their partners) and pass dims 64 + 64h .. 127 + 64h.
 template <int KS>
-__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params& P, int t) {
+__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P, int t) {
   const int r = t & 127, h = t >> 7;
+  const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
   // cos / sin of this key's offset from the tile's first key, two frequencies to a pair
   float2 oc[8], os[8];
 #pragma unroll
@@ -395,36 +398,41 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params
     oc[i] = make_float2(a.x, b.x);
     os[i] = make_float2(a.y, b.y);
   }
-  const double theta = t < kRopeDims / 2 ? P.theta[t] : 0.0;
   Walker walk(P);
   Unit w;
   __half2 amax = __floats2half2_rn(0.f, 0.f);
-  bool ok = true;
-#pragma unroll 1
-  for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
-    const uint32_t st = c % KS;
+  bool ok = true, more = walk.next_busy(P, w);
+  auto set_base = [&](uint32_t c) {  // the angles at unit c's first key
     if (t < kRopeDims / 2) {
-      const float2 a = angle(w.k0, theta);
+      const float2 a = angle(w.k0, P.theta[t]);
       C->k_cos[c & 1][t] = a.x;
       C->k_sin[c & 1][t] = a.y;
     }
-    if (ok) ok = wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
-    if (ok && c > 0) ok = wait(C, &C->lo_empty, (c - 1) & 1, P.wait_limit_ns);
-    // this tile's base angles written, those of two tiles back read; all leave together
+  };
+  if (more) set_base(0);
+#pragma unroll 1
+  for (uint32_t c = 0; more; ++c) {
+    const uint32_t st = c % KS, buf = c & 1;
+    ok = wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
+    if (ok && c >= 2) ok = wait(C, &C->k_free[buf], ((c >> 1) - 1) & 1, P.wait_limit_ns);
+    // this tile's base angles are written, those of the tile before are read; all leave together
     if (!named_bar_and(kRotBar, kRotThreads, ok)) break;
-    uint8_t* hi_row = smem + kRingOff + st * kStage + r * 128;
-    uint8_t* lo_row = smem + kLoOff + r * 128;
+    more = walk.next_busy(P, w);
+    if (more) set_base(c + 1);
+    tc_fence_after_sync();
+    const uint8_t* row = smem + st * kStage + r * 128;
+    const uint32_t dst = tmem + lane_base + kColK + 128u * buf;
+    uint32_t ah[8], al[8], bh[8], bl[8];  // dims 16h .. 16h + 15 and partners, two to a word
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int p = 2 * h + q;
-      const uint32_t ca = (p ^ (r & 7)) << 4, cb = ((p + 4) ^ (r & 7)) << 4;
-      const uint4 a = *reinterpret_cast<const uint4*>(hi_row + ca), b = *reinterpret_cast<const uint4*>(hi_row + cb);
+      const uint4 a = *reinterpret_cast<const uint4*>(row + ((p ^ (r & 7)) << 4));
+      const uint4 b = *reinterpret_cast<const uint4*>(row + (((p + 4) ^ (r & 7)) << 4));
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-      uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 bc = *reinterpret_cast<const float2*>(&C->k_cos[c & 1][8 * p + 2 * e]);
-        const float2 bs = *reinterpret_cast<const float2*>(&C->k_sin[c & 1][8 * p + 2 * e]);
+        const float2 bc = *reinterpret_cast<const float2*>(&C->k_cos[buf][8 * p + 2 * e]);
+        const float2 bs = *reinterpret_cast<const float2*>(&C->k_sin[buf][8 * p + 2 * e]);
         const float2 kc = oc[4 * q + e], ks = os[4 * q + e];
         const float2 cs = ffma2(bc, kc, fmul2(make_float2(-bs.x, -bs.y), ks));
         const float2 sn = ffma2(bs, kc, fmul2(bc, ks));
@@ -436,18 +444,27 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params
         const float2 m1 = make_float2(-1.f, -1.f);
         const float2 ul = ffma2(__half22float2(uh), m1, u), vl = ffma2(__half22float2(vh), m1, v);
         const __half2 uln = __floats2half2_rn(ul.x, ul.y), vln = __floats2half2_rn(vl.x, vl.y);
-        ah[e] = *reinterpret_cast<const uint32_t*>(&uh);
-        al[e] = *reinterpret_cast<const uint32_t*>(&uln);
-        bh[e] = *reinterpret_cast<const uint32_t*>(&vh);
-        bl[e] = *reinterpret_cast<const uint32_t*>(&vln);
+        ah[4 * q + e] = *reinterpret_cast<const uint32_t*>(&uh);
+        al[4 * q + e] = *reinterpret_cast<const uint32_t*>(&uln);
+        bh[4 * q + e] = *reinterpret_cast<const uint32_t*>(&vh);
+        bl[4 * q + e] = *reinterpret_cast<const uint32_t*>(&vln);
       }
-      *reinterpret_cast<uint4*>(hi_row + ca) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
-      *reinterpret_cast<uint4*>(hi_row + cb) = make_uint4(bh[0], bh[1], bh[2], bh[3]);
-      *reinterpret_cast<uint4*>(lo_row + ca) = make_uint4(al[0], al[1], al[2], al[3]);
-      *reinterpret_cast<uint4*>(lo_row + cb) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
     }
-    fence_proxy_async_smem();  // the fetcher's copies and these writes, before the MMA reads the stage
-    mbar_arrive(&C->k_full[st]);
+    tmem_st8(dst + 8 * h, ah);
+    tmem_st8(dst + 16 + 8 * h, bh);
+    tmem_st8(dst + 32 + 8 * h, al);
+    tmem_st8(dst + 48 + 8 * h, bl);
+    uint32_t pass[32];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + (1 + h) * kUnit + ((k ^ (r & 7)) << 4));
+      pass[4 * k] = v.x, pass[4 * k + 1] = v.y, pass[4 * k + 2] = v.z, pass[4 * k + 3] = v.w;
+    }
+    tmem_st32(dst + 64 + 32 * h, pass);
+    tmem_st_wait();
+    mbar_arrive(&C->k_empty[st]);  // the stage is read
+    tc_fence_before_sync();
+    mbar_arrive(&C->k_full[buf]);
   }
   const float2 top = __half22float2(amax);
   if (fmaxf(top.x, top.y) > 65504.f) atomicOr(&g_mimo_error, kErrRange);  // infinite: rounded past FP16's range
@@ -455,12 +472,13 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, const Params
 
 template <int KS, int QG>
 __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params& P, const CUtensorMap* tq, int lane) {
-  uint8_t* ring = smem + kRingOff + KS * kStage;
+  const uint32_t bytes = static_cast<uint32_t>(P.ntile) * 128u;  // a granule (a multiple of 1 KB where it is used twice)
+  const uint32_t stride = (bytes + 1023u) & ~1023u;
+  uint8_t* ring = smem + KS * kStage;
   Walker walk(P);
   Unit w;
   long long have = -1;
   uint32_t loads = 0, gi = 0;  // Q tiles, granules
-  const uint32_t bytes = static_cast<uint32_t>(P.ntile) * 128u;
   bool ok = true;
 #pragma unroll 1
   while (ok && walk.next_busy(P, w)) {
@@ -477,7 +495,7 @@ __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&C->q_full[st], bytes);
-          tma_load_2d(ring + st * kUnit, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
+          tma_load_2d(ring + st * stride, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
         }
         if (u == 0) {
           // the products that this granule waited for are two tiles back at most, and the sums two behind
@@ -497,9 +515,8 @@ __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params
 template <int KS, int QG>
 __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P) {
   const uint32_t idesc_f16 = make_idesc_f32acc(0, 0, 128, P.ntile), idesc_bf16 = make_idesc_f32acc(1, 0, 128, P.ntile);
-  constexpr uint32_t kStep = kUnit >> 4;
-  const uint32_t lo = sdesc_lo(smem_u32(smem + kLoOff), 16);
-  const uint32_t ring = smem_u32(smem + kRingOff + KS * kStage);
+  const uint32_t stride = (static_cast<uint32_t>(P.ntile) * 128u + 1023u) & ~1023u;
+  const uint32_t ring = smem_u32(smem + KS * kStage);
   Walker walk(P);
   Unit w;
   long long have = -1;
@@ -507,9 +524,9 @@ __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, 
   bool any = false;
 #pragma unroll 1
   for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
-    const uint32_t st = c % KS;
-    if (!wait(C, &C->k_full[st], (c / KS) & 1, P.wait_limit_ns)) return;
-    const uint32_t hi = sdesc_lo(smem_u32(smem + kRingOff + st * kStage), 16);
+    const uint32_t buf = c & 1;
+    if (!wait(C, &C->k_full[buf], (c >> 1) & 1, P.wait_limit_ns)) return;
+    const uint32_t k = tmem + kColK + 128u * buf;  // columns: hi 0, lo 32, pass 64 and 96
 #pragma unroll 1
     for (int qt = w.qt0; qt < w.qt1; ++qt, ++d) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
@@ -521,29 +538,26 @@ __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, 
       }
       have = row;
       any = true;
-      const bool last = qt + 1 == w.qt1;
       if (d >= 2 && !wait(C, &C->s_empty[d & 1], ((d >> 1) - 1) & 1, P.wait_limit_ns)) return;
       const uint32_t acc = tmem + 128u * (d & 1);
-      // granule u of the tile: Q hi with K lo and K hi, Q lo with K hi, then the pass-through dims
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      // five products of 64 dims: Q hi with K hi and K lo, Q lo with K hi, pass with pass.  A loop, so that its
+      // few instructions stay in the instruction cache beside the other roles'.
+#pragma unroll 1
+      for (int i = 0; i < 5; ++i) {
+        const int u = i > 0 ? i - 1 : 0;  // granule
         const uint32_t slot = (gi + u) % QG;
-        if (fresh && !wait(C, &C->q_full[slot], ((gi + u) / QG) & 1, P.wait_limit_ns)) return;
-        if (u == 0 || fresh) tc_fence_after_sync();
-        const uint32_t q = sdesc_lo(ring + slot * kUnit, 16);
-        if (u == 0) {
+        if (fresh && i != 1 && !wait(C, &C->q_full[slot], ((gi + u) / QG) & 1, P.wait_limit_ns)) return;
+        tc_fence_after_sync();
+        const uint32_t q = sdesc_lo(ring + slot * stride, 16);
+        const uint32_t a = k + (i == 1 ? 32u : i < 3 ? 0u : 32u * (i - 1));
+        const uint32_t idesc = i < 3 ? idesc_f16 : idesc_bf16;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss_lo(acc, lo + 2 * k, q + 2 * k, idesc_f16, k > 0 ? 1u : 0u);
-          if (last) tc_commit(&C->lo_empty);
-        }
-        const uint32_t a = hi + (u < 2 ? 0u : (u - 1) * kStep);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ss_lo(acc, a + 2 * k, q + 2 * k, u < 2 ? idesc_f16 : idesc_bf16, 1u);
-        if (QG > 4) tc_commit(&C->q_empty[slot]);
+        for (int s = 0; s < 4; ++s) mma_ts_lo(acc, a + 8 * s, q + 2 * s, idesc, i + s > 0 ? 1u : 0u);
+        if (QG > 4 && i > 0) tc_commit(&C->q_empty[slot]);
       }
       tc_commit(&C->s_full[d & 1]);
     }
-    tc_commit(&C->k_empty[st]);
+    tc_commit(&C->k_free[buf]);
   }
 }
 
@@ -637,7 +651,7 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
 template <int KS, int QG>
 __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_constant__ CUtensorMap tq,
                                                               const __grid_constant__ Params P) {
-  static_assert(KS <= kMaxKS && QG <= kMaxQG && kRingOff + KS * kStage + QG * kUnit <= kCtrlOff, "rings");
+  static_assert(KS <= kMaxKS && QG <= kMaxQG, "rings");  // the granules' size goes by ntile: the launch checks it
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctrl* C = reinterpret_cast<Ctrl*>(smem + kCtrlOff);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -650,15 +664,15 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) {
       mbar_init(&C->k_landed[s], 128);  // one cp.async arrival per fetcher thread
-      mbar_init(&C->k_full[s], kRotThreads);
-      mbar_init(&C->k_empty[s], 1);
+      mbar_init(&C->k_empty[s], kRotThreads);
     }
-    mbar_init(&C->lo_empty, 1);
     for (int s = 0; s < QG; ++s) {
       mbar_init(&C->q_full[s], 1);
       mbar_init(&C->q_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&C->k_full[s], kRotThreads);
+      mbar_init(&C->k_free[s], 1);
       mbar_init(&C->s_full[s], 1);
       mbar_init(&C->s_empty[s], 128);
     }
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
   } else if (warp < 8) {
     role_fetch<KS>(smem, C, P, tid - 128);
   } else if (warp < 16) {
-    role_rotate<KS>(smem, C, P, tid - 256);
+    role_rotate<KS>(smem, C, tmem, P, tid - 256);
   } else if (warp == 16) {
     if ((tid & 31) == 0) role_mma<KS, QG>(smem, C, tmem, P);
   } else {

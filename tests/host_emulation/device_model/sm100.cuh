@@ -480,6 +480,11 @@ inline void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   const uint32_t lane = (taddr >> 16) + hemu::lin_tid() % 32, col = taddr & 0xFFFFu;
   for (int j = 0; j < 16; ++j) g_tmem_all[hemu::g_cur_cta][lane][col + j] = r[j];
 }
+inline void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  tmem_lane_check(taddr);
+  const uint32_t lane = (taddr >> 16) + hemu::lin_tid() % 32, col = taddr & 0xFFFFu;
+  for (int j = 0; j < 8; ++j) g_tmem_all[hemu::g_cur_cta][lane][col + j] = r[j];
+}
 inline void tmem_st_wait() {}
 
 // ---------------------------------------------------------------- warp-group helpers
