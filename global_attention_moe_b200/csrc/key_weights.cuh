@@ -29,16 +29,15 @@
 //   warps 4-7   K fetcher: gathers the tile's rows by index with cp.async into the 128-byte-swizzled layout
 //   warps 8-15  K rotation, two threads to a key: rows from shared memory, BF16 -> FP16 hi and lo (angle
 //               addition from the tile's first key; paired FP32 arithmetic), into TMEM with the pass dims
-//   warp 16     TMEM owner; lane 0 issues the MMAs (A = K from TMEM, B = Q from shared memory)
+//   warp 16     TMEM owner; issues the MMAs (A = K from TMEM, B = Q from shared memory)
 //   warp 17     Q loader: TMA boxes of the prepared rows, and their lse
 // Units are walked in order by every role.  A gathered K tile (48 KB) stays in its stage only until it has been
 // rotated into one of two TMEM buffers (128 columns: hi, lo, pass): the gather's latency, about 2.5 us for rows
 // spread over the cache, is what has to be covered, and the stages are what covers it.  It also leaves the
 // tensor cores one operand to read from shared memory instead of two, whose 128 bytes a cycle they would
-// take whole.  Q tiles go through granules of ntile rows x 64 dims (hi, lo, pass, pass).  With one query tile
-// per sequence (decode steps) a CTA takes a contiguous run of units, so Q stays in its four granules while
-// the keys of a (sequence, KV head) stream through KS stages; with more (chunked prefill) a key tile stays in
-// TMEM while the query tiles stream through two sets of granules.
+// take whole.  With one query tile per sequence (decode steps, QS = 1) a CTA takes a contiguous run of units, so
+// the Q tile stays in shared memory while the keys of a (sequence, KV head) stream through KS stages; with more
+// (chunked prefill, QS = 2) a key tile stays in TMEM while the query tiles stream through two Q stages.
 #pragma once
 
 #include "attn_decode.cuh"
@@ -51,13 +50,13 @@ constexpr int kThreads = 576;
 constexpr int kTile = 128;             // keys per unit
 constexpr uint32_t kUnit = 16384;      // 128 rows x 64 dims x 2 B
 constexpr uint32_t kStage = 3 * kUnit;  // a gathered K tile: dims 0..63, 64..127, 128..191
-constexpr uint32_t kCtrlOff = 14 * kUnit;  // KS stages, then QG granules
+constexpr uint32_t kCtrlOff = 14 * kUnit;  // KS stages, then QS Q tiles
 constexpr int kLseSlots = 4;
 constexpr uint32_t kTmemCols = 512;        // two score tiles of at most 128 columns, then two K tiles
 constexpr uint32_t kColK = 256;
 constexpr uint32_t kRotBar = 1;            // named barrier of the rotation warps
 constexpr int kRotThreads = 256;
-constexpr int kMaxKS = 4, kMaxQG = 8;
+constexpr int kMaxKS = 4;
 constexpr int kMaxSplits = 16;
 
 struct Params {
@@ -225,7 +224,7 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
 struct Ctrl {
   uint64_t k_landed[kMaxKS], k_empty[kMaxKS];  // stages
   uint64_t k_full[2], k_free[2];               // K tiles in TMEM
-  uint64_t q_full[kMaxQG], q_empty[kMaxQG];
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint64_t lse_full[kLseSlots];
   uint32_t tmem_base;
@@ -386,7 +385,7 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
 
 // Thread: key r = t % 128 of the tile (the TMEM lane), h = t / 128: chunk pairs 2h and 2h + 1 (dims 16h ..
 // 16h + 15 and their partners) and pass dims 64 + 64h .. 127 + 64h.
-template <int KS>
+template <int KS, int QS>
 __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P, int t) {
   const int r = t & 127, h = t >> 7;
   const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
@@ -414,7 +413,8 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tme
   for (uint32_t c = 0; more; ++c) {
     const uint32_t st = c % KS, buf = c & 1;
     ok = wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
-    if (ok && c >= 2) ok = wait(C, &C->k_free[buf], ((c >> 1) - 1) & 1, P.wait_limit_ns);
+    // the products with the tile before last are done: with one query tile to a unit its score tile says so
+    if (ok && c >= 2) ok = wait(C, QS == 1 ? &C->s_full[buf] : &C->k_free[buf], ((c >> 1) - 1) & 1, P.wait_limit_ns);
     // this tile's base angles are written, those of the tile before are read; all leave together
     if (!named_bar_and(kRotBar, kRotThreads, ok)) break;
     more = walk.next_busy(P, w);
@@ -470,94 +470,105 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tme
   if (fmaxf(top.x, top.y) > 65504.f) atomicOr(&g_mimo_error, kErrRange);  // infinite: rounded past FP16's range
 }
 
-template <int KS, int QG>
+template <int KS, int QS>
 __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params& P, const CUtensorMap* tq, int lane) {
-  const uint32_t bytes = static_cast<uint32_t>(P.ntile) * 128u;  // a granule (a multiple of 1 KB where it is used twice)
-  const uint32_t stride = (bytes + 1023u) & ~1023u;
+  const uint32_t unit = static_cast<uint32_t>(P.ntile) * 128u;  // 64 dims of the tile's rows: a multiple of 2 KB
   uint8_t* ring = smem + KS * kStage;
   Walker walk(P);
   Unit w;
   long long have = -1;
-  uint32_t loads = 0, gi = 0;  // Q tiles, granules
+  uint32_t loads = 0;
   bool ok = true;
 #pragma unroll 1
   while (ok && walk.next_busy(P, w)) {
 #pragma unroll 1
-    for (int qt = w.qt0; ok && qt < w.qt1; ++qt) {
+    for (int qt = w.qt0; qt < w.qt1; ++qt) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
-      if (QG == 4 && row == have) continue;  // with more granules each use hands them back
+      if (QS == 1 && row == have) continue;
       have = row;
-#pragma unroll 1
-      for (int u = 0; u < 4; ++u, ++gi) {
-        const uint32_t st = gi % QG;
-        ok = gi < QG || wait(C, &C->q_empty[st], (gi / QG - 1) & 1, P.wait_limit_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&C->q_full[st], bytes);
-          tma_load_2d(ring + st * stride, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
-        }
-        if (u == 0) {
-          // the products that this granule waited for are two tiles back at most, and the sums two behind
-          // those, so the slot's last reader is done
-          for (int c = lane; c < P.ntile; c += 32)
-            C->lse2[loads % kLseSlots][c] = qt * P.ntile + c < w.rows ? __ldg(P.lse2 + row + c) : 0.f;
-          mbar_arrive(&C->lse_full[loads % kLseSlots]);
-        }
+      const uint32_t st = loads % QS;
+      ok = loads < QS || wait(C, &C->q_empty[st], (loads / QS - 1) & 1, P.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // the products that this stage waited for are QS tiles back, and the sums two behind those: the slot's
+      // last reader is done
+      for (int c = lane; c < P.ntile; c += 32)
+        C->lse2[loads % kLseSlots][c] = qt * P.ntile + c < w.rows ? __ldg(P.lse2 + row + c) : 0.f;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&C->q_full[st], 4 * unit);
+        for (int u = 0; u < 4; ++u)
+          tma_load_2d(ring + (4 * st + u) * unit, tq, &C->q_full[st], 64 * u, static_cast<int32_t>(row));
       }
-      if (ok) ++loads;
+      mbar_arrive(&C->lse_full[loads % kLseSlots]);
+      ++loads;
     }
   }
   // nothing of ours stays in flight, on every path
-  for (uint32_t i = gi > QG ? gi - QG : 0; i < gi; ++i) wait(C, &C->q_full[i % QG], (i / QG) & 1, P.wait_limit_ns);
+  for (uint32_t i = loads > QS ? loads - QS : 0; i < loads; ++i)
+    wait(C, &C->q_full[i % QS], (i / QS) & 1, P.wait_limit_ns);
 }
 
-template <int KS, int QG>
+// S = K Q^T of one tile: Q hi with K hi and K lo, Q lo with K hi, pass with pass.  k: K's TMEM columns (hi 0, lo
+// 32, pass 64 and 96); q: Q's descriptor (hi, lo, pass, pass, qu apart).  All 20 in a row: the issue of an MMA
+// from a rolled loop takes about 250 cycles, in a row about 90.
+__device__ __forceinline__ void issue_tile(uint32_t acc, uint32_t k, uint32_t q, uint32_t qu, uint32_t idesc_f16,
+                                           uint32_t idesc_bf16) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + 2 * s, idesc_f16, s > 0 ? 1u : 0u);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 32 + 8 * s, q + 2 * s, idesc_f16, 1u);
+  q += qu;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + 2 * s, idesc_f16, 1u);
+  q += qu;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 64 + 8 * s, q + 2 * s, idesc_bf16, 1u);
+  q += qu;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 96 + 8 * s, q + 2 * s, idesc_bf16, 1u);
+}
+
+// The whole warp walks the units and waits; one lane issues.  What the MMAs' operands are formed from is made
+// uniform over the warp first, so that they are formed in the uniform registers that the MMAs read.
+template <int KS, int QS>
 __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P) {
   const uint32_t idesc_f16 = make_idesc_f32acc(0, 0, 128, P.ntile), idesc_bf16 = make_idesc_f32acc(1, 0, 128, P.ntile);
-  const uint32_t stride = (static_cast<uint32_t>(P.ntile) * 128u + 1023u) & ~1023u;
-  const uint32_t ring = smem_u32(smem + KS * kStage);
+  const uint32_t unit = static_cast<uint32_t>(P.ntile) * 128u;
+  const uint32_t q0 = sdesc_lo(smem_u32(smem + KS * kStage), 16), qu = unit >> 4;
+  const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
   Walker walk(P);
   Unit w;
   long long have = -1;
-  uint32_t gi = 0, d = 0;  // granules of the Q tiles before the current one; score tiles
-  bool any = false;
+  uint32_t loads = 0, d = 0;
 #pragma unroll 1
   for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
     const uint32_t buf = c & 1;
-    if (!wait(C, &C->k_full[buf], (c >> 1) & 1, P.wait_limit_ns)) return;
-    const uint32_t k = tmem + kColK + 128u * buf;  // columns: hi 0, lo 32, pass 64 and 96
+    if (!__all_sync(0xffffffffu, wait(C, &C->k_full[buf], (c >> 1) & 1, P.wait_limit_ns))) return;
 #pragma unroll 1
     for (int qt = w.qt0; qt < w.qt1; ++qt, ++d) {
       const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
-      const bool fresh = QG > 4 || row != have;
-      if (fresh && any) {  // the last product with the rows before is issued: hand them back
-        if (QG == 4)
-          for (int u = 0; u < 4; ++u) tc_commit(&C->q_empty[u]);
-        gi += 4;
+      bool ok = true;
+      if (QS > 1 || row != have) {
+        // a commit takes about 50 cycles of the tensor pipe: one stage is handed back only where Q changes
+        if (QS == 1 && loads > 0 && elect_one()) tc_commit(&C->q_empty[0]);
+        have = row;
+        ok = wait(C, &C->q_full[loads % QS], (loads / QS) & 1, P.wait_limit_ns);
+        ++loads;
       }
-      have = row;
-      any = true;
-      if (d >= 2 && !wait(C, &C->s_empty[d & 1], ((d >> 1) - 1) & 1, P.wait_limit_ns)) return;
-      const uint32_t acc = tmem + 128u * (d & 1);
-      // five products of 64 dims: Q hi with K hi and K lo, Q lo with K hi, pass with pass.  A loop, so that its
-      // few instructions stay in the instruction cache beside the other roles'.
-#pragma unroll 1
-      for (int i = 0; i < 5; ++i) {
-        const int u = i > 0 ? i - 1 : 0;  // granule
-        const uint32_t slot = (gi + u) % QG;
-        if (fresh && i != 1 && !wait(C, &C->q_full[slot], ((gi + u) / QG) & 1, P.wait_limit_ns)) return;
-        tc_fence_after_sync();
-        const uint32_t q = sdesc_lo(ring + slot * stride, 16);
-        const uint32_t a = k + (i == 1 ? 32u : i < 3 ? 0u : 32u * (i - 1));
-        const uint32_t idesc = i < 3 ? idesc_f16 : idesc_bf16;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) mma_ts_lo(acc, a + 8 * s, q + 2 * s, idesc, i + s > 0 ? 1u : 0u);
-        if (QG > 4 && i > 0) tc_commit(&C->q_empty[slot]);
+      if (ok && d >= 2) ok = wait(C, &C->s_empty[d & 1], ((d >> 1) - 1) & 1, P.wait_limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      tc_fence_after_sync();
+      const uint32_t st = __shfl_sync(0xffffffffu, (loads - 1) % QS, 0);
+      const uint32_t acc = t0 + __shfl_sync(0xffffffffu, 128u * (d & 1), 0);
+      const uint32_t k = t0 + __shfl_sync(0xffffffffu, kColK + 128u * buf, 0);
+      if (elect_one()) {
+        issue_tile(acc, k, q0 + 4 * st * qu, qu, idesc_f16, idesc_bf16);
+        tc_commit(&C->s_full[d & 1]);
+        if (QS > 1) tc_commit(&C->q_empty[st]);
+        if (QS > 1 && qt + 1 == w.qt1) tc_commit(&C->k_free[buf]);
       }
-      tc_commit(&C->s_full[d & 1]);
+      __syncwarp();
     }
-    tc_commit(&C->k_free[buf]);
   }
 }
 
@@ -648,10 +659,10 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
   }
 }
 
-template <int KS, int QG>
+template <int KS, int QS>
 __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_constant__ CUtensorMap tq,
                                                               const __grid_constant__ Params P) {
-  static_assert(KS <= kMaxKS && QG <= kMaxQG, "rings");  // the granules' size goes by ntile: the launch checks it
+  static_assert(KS <= kMaxKS, "stages");  // what Q takes goes by ntile: the launch keeps to kCtrlOff
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctrl* C = reinterpret_cast<Ctrl*>(smem + kCtrlOff);
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -666,11 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
       mbar_init(&C->k_landed[s], 128);  // one cp.async arrival per fetcher thread
       mbar_init(&C->k_empty[s], kRotThreads);
     }
-    for (int s = 0; s < QG; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&C->q_full[s], 1);
       mbar_init(&C->q_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&C->k_full[s], kRotThreads);
       mbar_init(&C->k_free[s], 1);
       mbar_init(&C->s_full[s], 1);
@@ -693,11 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
   } else if (warp < 8) {
     role_fetch<KS>(smem, C, P, tid - 128);
   } else if (warp < 16) {
-    role_rotate<KS>(smem, C, tmem, P, tid - 256);
+    role_rotate<KS, QS>(smem, C, tmem, P, tid - 256);
   } else if (warp == 16) {
-    if ((tid & 31) == 0) role_mma<KS, QG>(smem, C, tmem, P);
+    role_mma<KS, QS>(smem, C, tmem, P);
   } else {
-    role_load_q<KS, QG>(smem, C, P, &tq, tid & 31);
+    role_load_q<KS, QS>(smem, C, P, &tq, tid & 31);
   }
   __syncwarp();
   tc_fence_before_sync();

@@ -195,11 +195,11 @@ bool key_weights_ready(int dev) {
   static std::atomic<int> state[64];  // 0 unknown, 1 ready, -1 failed
   if (dev < 0 || dev >= 64) return false;
   if (state[dev].load() == 0)
-    state[dev].store(cudaFuncSetAttribute(kw::kw_main_kernel<4, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    state[dev].store(cudaFuncSetAttribute(kw::kw_main_kernel<4, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           kw::kSmemBytes) == cudaSuccess &&
-                             cudaFuncSetAttribute(kw::kw_main_kernel<3, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             cudaFuncSetAttribute(kw::kw_main_kernel<3, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   kw::kSmemBytes) == cudaSuccess &&
-                             cudaFuncSetAttribute(kw::kw_main_kernel<2, 8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             cudaFuncSetAttribute(kw::kw_main_kernel<2, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   kw::kSmemBytes) == cudaSuccess
                          ? 1
                          : -1);
@@ -915,13 +915,13 @@ int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const 
     if (!encode_2d(&tq, P.qs, 256, (uint64_t)d->total_q * P.hq, (uint32_t)P.ntile)) return MIMO_ERR_CUDA;
     const long long units = ((long long)d->total_kv / kw::kTile + d->num_seqs) * P.hkv * P.splits;
     const unsigned grid = (unsigned)std::min<long long>(units, info->sms);
-    // K stages and Q granules within 224 KB: 4 x 48 + 4 x 8, 3 x 48 + 4 x 16, 2 x 48 + 8 x 16
+    // K stages of 48 KB and Q tiles of ntile / 2 KB within 224 KB
     if (P.contiguous && P.ntile <= 64)
-      kw::kw_main_kernel<4, 4><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+      kw::kw_main_kernel<4, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     else if (P.contiguous)
-      kw::kw_main_kernel<3, 4><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+      kw::kw_main_kernel<3, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     else
-      kw::kw_main_kernel<2, 8><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
+      kw::kw_main_kernel<2, 2><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     if (cudaGetLastError() != cudaSuccess) return MIMO_ERR_CUDA;
   }
   kw::kw_join_kernel<<<(unsigned)(((long long)d->total_kv + kw::kJoinThreads - 1) / kw::kJoinThreads),

@@ -566,4 +566,6 @@ inline float rcp_approx(float x) {
 
 inline float2 fmul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 
+inline bool elect_one() { return hemu::lin_tid() % 32 == 0; }
+
 }  // namespace mimo
