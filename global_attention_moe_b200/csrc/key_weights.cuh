@@ -24,13 +24,15 @@
 //      head][key];
 //   3. kw_join_kernel: adds the partial rows in a fixed order, and prev.
 //
-// Warp roles of the main kernel (18 warps):
-//   warps 0-3   sums (thread = key = TMEM lane)
-//   warps 4-7   K fetcher: gathers the tile's rows by index with cp.async into the 128-byte-swizzled layout
-//   warps 8-15  K rotation, two threads to a key: rows from shared memory, BF16 -> FP16 hi and lo (angle
-//               addition from the tile's first key; paired FP32 arithmetic), into TMEM with the pass dims
-//   warp 16     TMEM owner; issues the MMAs (A = K from TMEM, B = Q from shared memory)
-//   warp 17     Q loader: TMA boxes of the prepared rows, and their lse
+// Warp roles of the main kernel (24 warps; registers are dealt out by warpgroup):
+//   warp 0       TMEM owner; issues the MMAs (A = K from TMEM, B = Q from shared memory)
+//   warp 1       Q loader: TMA boxes of the prepared rows, and their lse
+//   warp 2       angles of the key tiles' first positions
+//   warps 4-11   sums (thread = key = TMEM lane): two groups of four that take the score tiles in turn, since
+//                one group's sums take longer than a tile's products (1550 cycles)
+//   warps 12-19  K rotation, two threads to a key: rows from shared memory, BF16 -> FP16 hi and lo (angle
+//                addition from the tile's first key; paired FP32 arithmetic), into TMEM with the pass dims
+//   warps 20-23  K fetcher: gathers the tile's rows by index with cp.async into the 128-byte-swizzled layout
 // Units are walked in order by every role.  A gathered K tile (48 KB) stays in its stage only until it has been
 // rotated into one of two TMEM buffers (128 columns: hi, lo, pass): the gather's latency, about 2.5 us for rows
 // spread over the cache, is what has to be covered, and the stages are what covers it.  It also leaves the
@@ -46,7 +48,7 @@
 namespace mimo {
 namespace kw {
 
-constexpr int kThreads = 576;
+constexpr int kThreads = 768;
 constexpr int kTile = 128;             // keys per unit
 constexpr uint32_t kUnit = 16384;      // 128 rows x 64 dims x 2 B
 constexpr uint32_t kStage = 3 * kUnit;  // a gathered K tile: dims 0..63, 64..127, 128..191
@@ -54,8 +56,9 @@ constexpr uint32_t kCtrlOff = 14 * kUnit;  // KS stages, then QS Q tiles
 constexpr int kLseSlots = 4;
 constexpr uint32_t kTmemCols = 512;        // two score tiles of at most 128 columns, then two K tiles
 constexpr uint32_t kColK = 256;
-constexpr uint32_t kRotBar = 1;            // named barrier of the rotation warps
 constexpr int kRotThreads = 256;
+// registers of a thread, by warpgroup: 80 at launch; 2 x (56 + 72 + 112) = 6 x 80
+constexpr uint32_t kRegsSmall = 56, kRegsSum = 72, kRegsRotate = 112;
 constexpr int kMaxKS = 4;
 constexpr int kMaxSplits = 16;
 
@@ -71,11 +74,12 @@ struct Params {
   uint16_t* qs;               // workspace: [hkv * Tq * group, 256]
   float* lse2;                // workspace: [hkv * Tq * group], log2 units
   long long* units;           // workspace: [num_seqs + 1], running count of units
-  float* partial;             // workspace: [splits * hkv, total_kv]
+  float* partial;             // workspace: [parts * hkv, total_kv]
   int32_t num_seqs, total_q, total_kv, cache_rows, max_q_len, max_kv_len;
   int32_t hq, hkv, group;
   int32_t window;             // < 0: global causal layer
   int32_t splits;             // parts of the query tiles
+  int32_t parts;              // partial rows to a KV head: 1, or two to a split
   int32_t ntile;              // query rows per tile (MMA N): multiple of 16, at most 128
   int32_t contiguous;         // a CTA's units: a run (1) or every gridDim-th (0)
   float scale_log2;
@@ -108,8 +112,8 @@ __device__ __forceinline__ bool load_seq(const Params& P, int b, Seq& s) {
   return true;
 }
 
-// cos / sin of pos theta, the angle reduced in FP64 (out of line: every copy of sincosf is a few KB of code).
-__device__ __noinline__ float2 angle(int pos, double theta) {
+// cos / sin of pos theta, the angle reduced in FP64.
+__device__ __forceinline__ float2 angle(int pos, double theta) {
   const double a = static_cast<double>(pos) * theta;
   const double n = rint(a * kInvTwoPi);
   float s, c;
@@ -224,6 +228,7 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
 struct Ctrl {
   uint64_t k_landed[kMaxKS], k_empty[kMaxKS];  // stages
   uint64_t k_full[2], k_free[2];               // K tiles in TMEM
+  uint64_t a_full[2], a_empty[2];              // angles of a tile's first key
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint64_t lse_full[kLseSlots];
@@ -383,45 +388,53 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   if (bad) atomicOr(&g_mimo_error, kErrSeqlens);
 }
 
+// Cos / sin of every frequency (lane) at each tile's first key, one tile ahead of the rotation.
+__device__ __forceinline__ void role_angles(Ctrl* C, const Params& P, int lane) {
+  const double theta = P.theta[lane];
+  Walker walk(P);
+  Unit w;
+#pragma unroll 1
+  for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
+    const uint32_t buf = c & 1;
+    const float2 a = angle(w.k0, theta);
+    if (c >= 2 && !wait(C, &C->a_empty[buf], ((c >> 1) - 1) & 1, P.wait_limit_ns)) return;
+    C->k_cos[buf][lane] = a.x;
+    C->k_sin[buf][lane] = a.y;
+    mbar_arrive(&C->a_full[buf]);
+  }
+}
+
 // Thread: key r = t % 128 of the tile (the TMEM lane), h = t / 128: chunk pairs 2h and 2h + 1 (dims 16h ..
-// 16h + 15 and their partners) and pass dims 64 + 64h .. 127 + 64h.
+// 16h + 15 and their partners) and pass dims 64 + 64h .. 127 + 64h.  oc, os: cos / sin of the key's offset from
+// the tile's first key for those dims, two frequencies to a pair.
 template <int KS, int QS>
-__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P, int t) {
+__device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tmem, const Params& P, int t,
+                                            const float2 (&oc)[8], const float2 (&os)[8]) {
   const int r = t & 127, h = t >> 7;
   const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
-  // cos / sin of this key's offset from the tile's first key, two frequencies to a pair
-  float2 oc[8], os[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 a = angle(r, P.theta[16 * h + 2 * i]), b = angle(r, P.theta[16 * h + 2 * i + 1]);
-    oc[i] = make_float2(a.x, b.x);
-    os[i] = make_float2(a.y, b.y);
-  }
   Walker walk(P);
   Unit w;
   __half2 amax = __floats2half2_rn(0.f, 0.f);
-  bool ok = true, more = walk.next_busy(P, w);
-  auto set_base = [&](uint32_t c) {  // the angles at unit c's first key
-    if (t < kRopeDims / 2) {
-      const float2 a = angle(w.k0, P.theta[t]);
-      C->k_cos[c & 1][t] = a.x;
-      C->k_sin[c & 1][t] = a.y;
-    }
-  };
-  if (more) set_base(0);
 #pragma unroll 1
-  for (uint32_t c = 0; more; ++c) {
+  for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
     const uint32_t st = c % KS, buf = c & 1;
-    ok = wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
+    bool ok = wait(C, &C->a_full[buf], (c >> 1) & 1, P.wait_limit_ns);
+    ok = ok && wait(C, &C->k_landed[st], (c / KS) & 1, P.wait_limit_ns);
     // the products with the tile before last are done: with one query tile to a unit its score tile says so
     if (ok && c >= 2) ok = wait(C, QS == 1 ? &C->s_full[buf] : &C->k_free[buf], ((c >> 1) - 1) & 1, P.wait_limit_ns);
-    // this tile's base angles are written, those of the tile before are read; all leave together
-    if (!named_bar_and(kRotBar, kRotThreads, ok)) break;
-    more = walk.next_busy(P, w);
-    if (more) set_base(c + 1);
+    if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
     const uint8_t* row = smem + st * kStage + r * 128;
     const uint32_t dst = tmem + lane_base + kColK + 128u * buf;
+    {
+      uint32_t pass[32];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + (1 + h) * kUnit + ((k ^ (r & 7)) << 4));
+        pass[4 * k] = v.x, pass[4 * k + 1] = v.y, pass[4 * k + 2] = v.z, pass[4 * k + 3] = v.w;
+      }
+      tmem_st32(dst + 64 + 32 * h, pass);
+    }
     uint32_t ah[8], al[8], bh[8], bl[8];  // dims 16h .. 16h + 15 and partners, two to a word
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -454,15 +467,9 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tme
     tmem_st8(dst + 16 + 8 * h, bh);
     tmem_st8(dst + 32 + 8 * h, al);
     tmem_st8(dst + 48 + 8 * h, bl);
-    uint32_t pass[32];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + (1 + h) * kUnit + ((k ^ (r & 7)) << 4));
-      pass[4 * k] = v.x, pass[4 * k + 1] = v.y, pass[4 * k + 2] = v.z, pass[4 * k + 3] = v.w;
-    }
-    tmem_st32(dst + 64 + 32 * h, pass);
     tmem_st_wait();
     mbar_arrive(&C->k_empty[st]);  // the stage is read
+    mbar_arrive(&C->a_empty[buf]);
     tc_fence_before_sync();
     mbar_arrive(&C->k_full[buf]);
   }
@@ -595,8 +602,11 @@ __device__ __forceinline__ void add_columns(const uint32_t (&s)[N], const float*
   }
 }
 
-__device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P, int r, int wq) {
-  const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+// Group grp takes the score tiles of its parity.  With one tile to a unit (QS = 1) it writes the whole sums of
+// its units; else each group writes its own partial row of every unit.
+template <int QS>
+__device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P, int r, uint32_t grp) {
+  const uint32_t acc = tmem + (static_cast<uint32_t>(r & ~31) << 16) + 128u * grp;
   const float sl2 = P.scale_log2;
   Walker walk(P);
   Unit w;
@@ -605,23 +615,22 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
 #pragma unroll 1
   while (walk.next(P, w)) {
     const int key = w.k0 + r;
+    // all queries of a tile see all keys of the unit from row see_all on, and up to row win_all
+    const long long see_all = (static_cast<long long>(w.k0) + w.nk - 1 - w.p0) * P.group;
+    const long long win_all = (static_cast<long long>(w.k0) + P.window + 1 - w.p0) * P.group;
     float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+    bool mine = false;
 #pragma unroll 1
     for (int qt = w.qt0; qt < w.qt1; ++qt, ++d) {
-      const long long row = w.row0 + static_cast<long long>(qt) * P.ntile;
-      bool ok = true;
-      if (row != have || !P.contiguous) {
-        // this load's lse; the loader is at most two loads ahead (its rows wait for the products of the
-        // loads before, and those for the score tiles), so the slot still holds it
-        have = row;
-        ok = wait(C, &C->lse_full[loads % kLseSlots], (loads / kLseSlots) & 1, P.wait_limit_ns);
+      const int base = qt * P.ntile;
+      if (QS > 1 || w.row0 + base != have) {
+        have = w.row0 + base;
         ++loads;
       }
-      const float* lse2 = C->lse2[(loads - 1) % kLseSlots];
-      const int base = qt * P.ntile, cols = min(P.ntile, w.rows - base);  // query rows of the tile
-      // the tile's first query sees the unit's last key, and the last one's window holds its first key
-      const bool all = w.p0 + base / P.group >= w.k0 + w.nk - 1 &&
-                       (P.window < 0 || w.k0 + P.window >= w.p0 + (base + cols - 1) / P.group);
+      if ((d & 1) != grp) continue;
+      mine = true;
+      const int cols = min(P.ntile, w.rows - base);  // query rows of the tile
+      const bool all = base >= see_all && (P.window < 0 || base + cols <= win_all);
       int c_lo = 0, c_hi = cols;
       if (!all) {  // columns (query rows) that see this key: a run
         const long long seen = (static_cast<long long>(key) - w.p0) * P.group - base;
@@ -631,9 +640,14 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
           c_hi = static_cast<int>(max(0LL, min(static_cast<long long>(cols), end)));
         }
       }
-      if (!__all_sync(0xffffffffu, ok && wait(C, &C->s_full[d & 1], (d >> 1) & 1, P.wait_limit_ns))) return;
+      // this load's lse; the loader is at most two loads ahead (its rows wait for the products of the loads
+      // before, and those for the score tiles), so the slot still holds it
+      const uint32_t slot = (loads - 1) % kLseSlots;
+      bool ok = wait(C, &C->lse_full[slot], ((loads - 1) / kLseSlots) & 1, P.wait_limit_ns);
+      ok = ok && wait(C, &C->s_full[grp], (d >> 1) & 1, P.wait_limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) return;
       tc_fence_after_sync();
-      const uint32_t acc = tmem + lane_base + 128u * (d & 1);
+      const float* lse2 = C->lse2[slot];
       int c0 = 0;
 #pragma unroll 1
       for (; c0 + 32 <= cols; c0 += 32) {
@@ -648,14 +662,16 @@ __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P
         uint32_t s[16];
         tmem_ld16(acc + c0, s);
         tmem_ld16_wait(s);
-        if (all && c0 + 16 <= cols) add_columns<16, false>(s, lse2 + c0, sl2, 0, 0, a0, a1);
-        else add_columns<16, true>(s, lse2 + c0, sl2, c_lo - c0, c_hi - c0, a0, a1);
+        add_columns<16, true>(s, lse2 + c0, sl2, c_lo - c0, c_hi - c0, a0, a1);
       }
       tc_fence_before_sync();
-      mbar_arrive(&C->s_empty[d & 1]);
+      mbar_arrive(&C->s_empty[grp]);
     }
-    if (r < w.nk)
-      P.partial[(static_cast<size_t>(w.f) * P.hkv + w.g) * P.total_kv + w.kv_beg + key] = (a0.x + a0.y) + (a1.x + a1.y);
+    if (r < w.nk && (QS > 1 || mine)) {
+      const int part = QS > 1 ? 2 * w.f + static_cast<int>(grp) : 0;
+      P.partial[(static_cast<size_t>(part) * P.hkv + w.g) * P.total_kv + w.kv_beg + key] =
+          (a0.x + a0.y) + (a1.x + a1.y);
+    }
   }
 }
 
@@ -682,6 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
       mbar_init(&C->q_empty[s], 1);
       mbar_init(&C->k_full[s], kRotThreads);
       mbar_init(&C->k_free[s], 1);
+      mbar_init(&C->a_full[s], 32);
+      mbar_init(&C->a_empty[s], kRotThreads);
       mbar_init(&C->s_full[s], 1);
       mbar_init(&C->s_empty[s], 128);
     }
@@ -689,29 +707,50 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     C->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 16) {
+  if (warp == 0) {
     tmem_alloc(&C->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  // cos / sin of every offset within a tile, by everyone into the rings' memory; the rotation's threads keep theirs
+  float2* table = reinterpret_cast<float2*>(smem);  // [offset][frequency]
+#pragma unroll 1
+  for (int i = tid; i < kTile * (kRopeDims / 2); i += kThreads)
+    table[i] = angle(i / (kRopeDims / 2), P.theta[i % (kRopeDims / 2)]);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = C->tmem_base;
+  float2 oc[8], os[8];
+  if (warp >= 12 && warp < 20) {
+    const int t = tid - 384;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&table[(t & 127) * (kRopeDims / 2) + 16 * (t >> 7) + 2 * i]);
+      oc[i] = make_float2(v.x, v.z);
+      os[i] = make_float2(v.y, v.w);
+    }
+  }
+  fence_proxy_async_smem();  // the Q tiles come by TMA into the same memory
+  __syncthreads();
   if (warp < 4) {
-    role_sum(C, tmem, P, tid, warp);
-  } else if (warp < 8) {
-    role_fetch<KS>(smem, C, P, tid - 128);
-  } else if (warp < 16) {
-    role_rotate<KS, QS>(smem, C, tmem, P, tid - 256);
-  } else if (warp == 16) {
-    role_mma<KS, QS>(smem, C, tmem, P);
+    setmaxnreg_dec<kRegsSmall>();
+    if (warp == 0) role_mma<KS, QS>(smem, C, tmem, P);
+    else if (warp == 1) role_load_q<KS, QS>(smem, C, P, &tq, tid & 31);
+    else if (warp == 2) role_angles(C, P, tid & 31);
+  } else if (warp < 12) {
+    setmaxnreg_dec<kRegsSum>();
+    role_sum<QS>(C, tmem, P, tid & 127, warp >= 8 ? 1u : 0u);
+  } else if (warp < 20) {
+    setmaxnreg_inc<kRegsRotate>();
+    role_rotate<KS, QS>(smem, C, tmem, P, tid - 384, oc, os);
   } else {
-    role_load_q<KS, QS>(smem, C, P, &tq, tid & 31);
+    setmaxnreg_dec<kRegsSmall>();
+    role_fetch<KS>(smem, C, P, tid - 640);
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 0) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -723,7 +762,7 @@ __global__ void __launch_bounds__(kJoinThreads) kw_join_kernel(const __grid_cons
   const long long i = static_cast<long long>(blockIdx.x) * kJoinThreads + threadIdx.x;
   const int lane = threadIdx.x & 31;
   const bool in = i < P.total_kv;
-  const int rows = P.splits * P.hkv;
+  const int rows = P.parts * P.hkv;
   // the partial rows are read before the entry's sequence is known: where no query sees the key they were not
   // written, and what is read does not count
   float v = 0.f;

@@ -843,7 +843,7 @@ constexpr int64_t kSmsForSplits = 148;  // the split of the query tiles, which s
 
 // Workspace layout (each part 256-byte aligned) and the split of the query tiles.
 struct KeyWeightsPlan {
-  int splits, ntile;
+  int splits, parts, ntile;
   bool contiguous;
   size_t qs, lse2, units, partial, bytes;
 };
@@ -858,12 +858,13 @@ KeyWeightsPlan key_weights_plan(const mimo_decode_dims* d) {
   const int64_t units = ((int64_t)d->total_kv / kw::kTile + d->num_seqs) * d->num_kv_heads;
   p.splits = (int)std::max<int64_t>(
       1, std::min({qtiles, (int64_t)kw::kMaxSplits, (4 * kSmsForSplits + units - 1) / units}));
+  p.parts = p.contiguous ? 1 : 2 * p.splits;
   const size_t qrows = (size_t)d->total_q * d->num_q_heads;
   p.qs = 0;
   p.lse2 = p.qs + align256(qrows * 512);
   p.units = p.lse2 + align256(qrows * 4);
   p.partial = p.units + align256(((size_t)d->num_seqs + 1) * 8);
-  p.bytes = p.partial + align256((size_t)p.splits * d->num_kv_heads * d->total_kv * 4);
+  p.bytes = p.partial + align256((size_t)p.parts * d->num_kv_heads * d->total_kv * 4);
   return p;
 }
 
@@ -901,6 +902,7 @@ int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const 
   P.group = d->num_q_heads / d->num_kv_heads;
   P.window = (layer_kind == MIMO_LAYER_GLOBAL) ? -1 : window;
   P.splits = plan.splits;
+  P.parts = plan.parts;
   P.ntile = plan.ntile;
   P.contiguous = plan.contiguous ? 1 : 0;
   P.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDimQK)));
