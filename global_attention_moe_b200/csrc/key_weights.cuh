@@ -57,8 +57,8 @@ constexpr int kLseSlots = 4;
 constexpr uint32_t kTmemCols = 512;        // two score tiles of at most 128 columns, then two K tiles
 constexpr uint32_t kColK = 256;
 constexpr int kRotThreads = 256;
-// registers of a thread, by warpgroup: 80 at launch; 2 x (56 + 72 + 112) = 6 x 80
-constexpr uint32_t kRegsSmall = 56, kRegsSum = 72, kRegsRotate = 112;
+// registers of a thread, by warpgroup: 80 at launch; 56 + 2 x 80 + 2 x 104 + 56 = 6 x 80
+constexpr uint32_t kRegsSmall = 56, kRegsRotate = 104, kRegsFetch = 56;
 constexpr int kMaxKS = 4;
 constexpr int kMaxSplits = 16;
 
@@ -249,55 +249,65 @@ struct Unit {
   long long row0;      // first prepared row of (KV head, sequence)
 };
 
-// The units of this CTA, in order.
+// The units of this CTA, in order: a run of them (QS = 1, one query tile to a sequence and one split), or every
+// gridDim-th.  Every role has its own walk in its loop, so the run's step is kept to a few instructions: the
+// roles' loops together have to fit the SM's instruction cache.
+template <int QS>
 struct Walker {
-  long long u, step, left;
-  int b = -1;
-  long long lo = 0, hi = 0;  // units of sequence b
-  int kt = 0, f = 0, g = 0, nq = 0;
+  long long u, left;
+  int b, kt, g, f, nq;
+  long long lo, hi;  // QS = 2: units of sequence b
   Seq s;
   __device__ __forceinline__ explicit Walker(const Params& P) {
     const long long total = P.units[P.num_seqs];
-    if (P.contiguous) {
+    if (QS == 1) {
       u = total * blockIdx.x / gridDim.x;
       left = total * (blockIdx.x + 1) / gridDim.x - u;
-      step = 1;
     } else {
       u = blockIdx.x;
-      step = gridDim.x;
-      left = u < total ? (total - u + step - 1) / step : 0;
+      left = u < total ? (total - u + gridDim.x - 1) / gridDim.x : 0;
     }
-    if (left > 0) {  // the sequence of the first unit
-      int a = 0, z = P.num_seqs;
-      while (z - a > 1) {
-        const int m = (a + z) / 2;
-        if (P.units[m] <= u) a = m;
-        else z = m;
-      }
-      b = a - 1;
+    b = kt = g = f = nq = 0;
+    lo = hi = 0;
+    if (left == 0) return;
+    int a = 0, z = P.num_seqs;  // the sequence of the first unit
+    while (z - a > 1) {
+      const int m = (a + z) / 2;
+      if (P.units[m] <= u) a = m;
+      else z = m;
+    }
+    b = a;
+    if (QS == 1) {
+      load_seq(P, b, s);
+      const int r = static_cast<int>(u - P.units[b]);
+      g = r / s.tiles;
+      kt = r - g * s.tiles;
+    } else {
+      --b;  // entered by the first step
     }
   }
   __device__ __forceinline__ bool next(const Params& P, Unit& w) {
     if (left == 0) return false;
-    bool place = step > 1 || u >= hi;  // else: the unit after the last one, in the same sequence
-    while (u >= hi) {
-      ++b;
-      lo = P.units[b];
-      hi = P.units[b + 1];
-      load_seq(P, b, s);
-      nq = (s.q_len * P.group + P.ntile - 1) / P.ntile;
-    }
-    if (place) {
+    --left;
+    if (QS == 1) {
+      while (g == P.hkv) {  // the next sequence that has units
+        load_seq(P, ++b, s);
+        kt = 0;
+        g = s.tiles > 0 ? 0 : P.hkv;
+      }
+    } else {
+      while (u >= hi) {
+        ++b;
+        lo = P.units[b];
+        hi = P.units[b + 1];
+        load_seq(P, b, s);
+        nq = (s.q_len * P.group + P.ntile - 1) / P.ntile;
+      }
       const int r = static_cast<int>(u - lo), r2 = r / s.tiles;
       kt = r - r2 * s.tiles;
       g = r2 / P.splits;
       f = r2 - g * P.splits;
-    } else if (++kt == s.tiles) {
-      kt = 0;
-      if (++f == P.splits) {
-        f = 0;
-        ++g;
-      }
+      u += gridDim.x;
     }
     w.f = f;
     w.g = g;
@@ -307,9 +317,15 @@ struct Walker {
     w.nk = min(kTile, s.kv_len - w.k0);
     w.p0 = s.kv_len - s.q_len;
     w.rows = s.q_len * P.group;
+    w.row0 = (static_cast<long long>(g) * P.total_q + s.q_beg) * P.group;
     w.qt0 = 0;
-    w.qt1 = nq;
-    if (!P.contiguous) {
+    w.qt1 = 1;
+    if (QS == 1) {
+      if (++kt == s.tiles) {
+        kt = 0;
+        ++g;
+      }
+    } else {
       w.qt0 = static_cast<int>(static_cast<long long>(nq) * f / P.splits);
       w.qt1 = static_cast<int>(static_cast<long long>(nq) * (f + 1) / P.splits);
       if (w.k0 > w.p0)  // causal: rows from the query at the tile's first key on
@@ -319,15 +335,12 @@ struct Walker {
         w.qt1 = static_cast<int>(min(static_cast<long long>(w.qt1), (end + P.ntile - 1) / P.ntile));
       }
     }
-    w.row0 = (static_cast<long long>(g) * P.total_q + s.q_beg) * P.group;
-    u += step;
-    --left;
     return true;
   }
   // The next unit that has query tiles.
   __device__ __forceinline__ bool next_busy(const Params& P, Unit& w) {
     while (next(P, w))
-      if (w.qt1 > w.qt0) return true;
+      if (QS == 1 || w.qt1 > w.qt0) return true;
     return false;
   }
 };
@@ -347,41 +360,57 @@ __device__ __forceinline__ bool wait(Ctrl* C, uint64_t* bar, uint32_t parity, ui
   }
 }
 
-__device__ __forceinline__ void load_idx(const Params& P, const Unit& w, int rsub, int (&idx)[8]) {
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int j = 16 * p + rsub;
-    idx[p] = j < w.nk ? __ldg(P.kv_indices + w.kv_beg + w.k0 + j) : -1;
-  }
-}
-
-template <int KS>
+// Warp wv gathers rows 32 wv .. 32 wv + 31 of each tile, lane l holding the cache row of the l-th (-1: none),
+// loaded two units ahead of its copies (its latency is about a unit's whole time).  A loop over the rows, four
+// at a time with eight lanes to a row, keeps the code short.
+template <int KS, int QS>
 __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params& P, int lt) {
-  const int l8 = lt & 7, rsub = lt >> 3;
-  Walker walk(P);
+  const int lane = lt & 31, row0 = lt & ~31, l8 = lane & 7, r4 = lane >> 3;
+  const size_t stride = static_cast<size_t>(P.hkv) * kHeadDimQK;
+  Walker<QS> walk(P);
   Unit w;
-  bool bad = false;
-  bool more = walk.next_busy(P, w);
-  int idx[8];
-  if (more) load_idx(P, w, rsub, idx);
-#pragma unroll 1
-  for (uint32_t c = 0; more; ++c) {
+  bool bad = false, more = true;
+  int row[3], g[3];  // of the unit to copy, and the next two
+  auto load = [&](int i) {
+    row[i] = -1;
+    g[i] = -1;
+    if (more) more = walk.next_busy(P, w);
+    if (!more) return;
+    g[i] = w.g;
+    if (row0 + lane < w.nk) {
+      row[i] = __ldg(P.kv_indices + w.kv_beg + w.k0 + row0 + lane);
+      if (row[i] < 0) row[i] = P.cache_rows;  // outside the cache on either side
+    }
+  };
+  uint32_t c = 0;
+  auto copy = [&](int i) -> bool {  // false at the end, or when the wait gave up
+    if (g[i] < 0) return false;
     const uint32_t st = c % KS;
-    if (c >= KS && !wait(C, &C->k_empty[st], (c / KS - 1) & 1, P.wait_limit_ns)) break;
-    const uint32_t dst = smem_u32(smem + st * kStage);
+    const bool ok = c < KS || wait(C, &C->k_empty[st], (c / KS - 1) & 1, P.wait_limit_ns);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const uint16_t* from = P.k_cache + g[i] * kHeadDimQK + 8 * l8;
+    uint32_t dst = smem_u32(smem + st * kStage) + static_cast<uint32_t>(row0 + r4) * 128u;
+#pragma unroll 1
+    for (int p = 0; p < 8; ++p, dst += 512) {
+      const int k = __shfl_sync(0xffffffffu, row[i], 4 * p + r4);
+      const bool in = k >= 0 && k < P.cache_rows;
+      bad |= k >= P.cache_rows;  // an index outside the cache: zeros, reported
+      const uint16_t* src = in ? from + static_cast<size_t>(k) * stride : P.k_cache;
+      const uint32_t nb = in ? 16u : 0u, at = dst + ((l8 ^ ((4 * p + r4) & 7)) << 4);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int j = 16 * p + rsub;
-      const bool in = idx[p] >= 0 && idx[p] < P.cache_rows;
-      bad |= j < w.nk && !in;  // an index outside the cache: zeros, reported
-      const uint16_t* src = in ? P.k_cache + (static_cast<size_t>(idx[p]) * P.hkv + w.g) * kHeadDimQK : P.k_cache;
-      const uint32_t sw = static_cast<uint32_t>(j * 128 + ((l8 ^ (j & 7)) << 4));
-#pragma unroll
-      for (int u = 0; u < 3; ++u) cp_async_16(dst + u * kUnit + sw, src + 64 * u + 8 * l8, in ? 16u : 0u);
+      for (int u = 0; u < 3; ++u) cp_async_16(at + u * kUnit, src + (in ? 64 * u : 0), nb);
     }
     cp_async_mbar_arrive_noinc(&C->k_landed[st]);
-    more = walk.next_busy(P, w);
-    if (more) load_idx(P, w, rsub, idx);  // in flight while this thread waits for the next stage
+    ++c;
+    load(i);
+    return true;
+  };
+  load(0);
+  load(1);
+  load(2);
+#pragma unroll 1
+  while (true) {  // the three sets by turns, so that none has to be moved before it has come
+    if (!copy(0) || !copy(1) || !copy(2)) break;  // the same for every lane
   }
   cp_async_commit();
   cp_async_wait<0>();  // nothing of ours stays in flight, on every path
@@ -389,9 +418,10 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
 }
 
 // Cos / sin of every frequency (lane) at each tile's first key, one tile ahead of the rotation.
+template <int QS>
 __device__ __forceinline__ void role_angles(Ctrl* C, const Params& P, int lane) {
   const double theta = P.theta[lane];
-  Walker walk(P);
+  Walker<QS> walk(P);
   Unit w;
 #pragma unroll 1
   for (uint32_t c = 0; walk.next_busy(P, w); ++c) {
@@ -412,7 +442,7 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tme
                                             const float2 (&oc)[8], const float2 (&os)[8]) {
   const int r = t & 127, h = t >> 7;
   const uint32_t lane_base = static_cast<uint32_t>(r & ~31) << 16;
-  Walker walk(P);
+  Walker<QS> walk(P);
   Unit w;
   __half2 amax = __floats2half2_rn(0.f, 0.f);
 #pragma unroll 1
@@ -481,7 +511,7 @@ template <int KS, int QS>
 __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params& P, const CUtensorMap* tq, int lane) {
   const uint32_t unit = static_cast<uint32_t>(P.ntile) * 128u;  // 64 dims of the tile's rows: a multiple of 2 KB
   uint8_t* ring = smem + KS * kStage;
-  Walker walk(P);
+  Walker<QS> walk(P);
   Unit w;
   long long have = -1;
   uint32_t loads = 0;
@@ -543,7 +573,7 @@ __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, 
   const uint32_t unit = static_cast<uint32_t>(P.ntile) * 128u;
   const uint32_t q0 = sdesc_lo(smem_u32(smem + KS * kStage), 16), qu = unit >> 4;
   const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
-  Walker walk(P);
+  Walker<QS> walk(P);
   Unit w;
   long long have = -1;
   uint32_t loads = 0, d = 0;
@@ -608,7 +638,7 @@ template <int QS>
 __device__ __forceinline__ void role_sum(Ctrl* C, uint32_t tmem, const Params& P, int r, uint32_t grp) {
   const uint32_t acc = tmem + (static_cast<uint32_t>(r & ~31) << 16) + 128u * grp;
   const float sl2 = P.scale_log2;
-  Walker walk(P);
+  Walker<QS> walk(P);
   Unit w;
   long long have = -1;
   uint32_t loads = 0, d = 0;
@@ -736,16 +766,15 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     setmaxnreg_dec<kRegsSmall>();
     if (warp == 0) role_mma<KS, QS>(smem, C, tmem, P);
     else if (warp == 1) role_load_q<KS, QS>(smem, C, P, &tq, tid & 31);
-    else if (warp == 2) role_angles(C, P, tid & 31);
+    else if (warp == 2) role_angles<QS>(C, P, tid & 31);
   } else if (warp < 12) {
-    setmaxnreg_dec<kRegsSum>();
     role_sum<QS>(C, tmem, P, tid & 127, warp >= 8 ? 1u : 0u);
   } else if (warp < 20) {
     setmaxnreg_inc<kRegsRotate>();
     role_rotate<KS, QS>(smem, C, tmem, P, tid - 384, oc, os);
   } else {
-    setmaxnreg_dec<kRegsSmall>();
-    role_fetch<KS>(smem, C, P, tid - 640);
+    setmaxnreg_dec<kRegsFetch>();
+    role_fetch<KS, QS>(smem, C, P, tid - 640);
   }
   __syncwarp();
   tc_fence_before_sync();
