@@ -131,7 +131,7 @@ __device__ __forceinline__ void split16(float x, __half& hi, __half& lo) {
 // Blocks 0 .. gridDim - 2: one warp per (token, kPrepHeads query heads), lane = RoPE pair; the rows are loaded
 // before the token's sequence is looked up.  Last block: the running count of units.
 constexpr int kPrepThreads = 256;
-constexpr int kPrepHeads = 8;
+constexpr int kPrepHeads = 4;
 
 // The last entry of the ascending list at most t (n >= 1 entries, the first taken as at most t), by a warp.
 __device__ __forceinline__ int find_seq(const int32_t* list, int n, int t, int lane) {
@@ -200,11 +200,15 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
   if (!ok) return;  // rows of no sequence are never read as queries
   const float2 cs = angle(s.kv_len - s.q_len + (t - s.q_beg), theta);
   float amax = 0.f;
+  int g = h0 / P.group, hh = h0 - g * P.group;  // KV head, head in the group
 #pragma unroll
   for (int i = 0; i < kPrepHeads; ++i)
     if (i < nh) {
-      const int h = h0 + i;
-      const size_t row = (static_cast<size_t>(h / P.group) * P.total_q + t) * P.group + h % P.group;
+      const size_t row = (static_cast<size_t>(g) * P.total_q + t) * P.group + hh;
+      if (++hh == P.group) {
+        hh = 0;
+        ++g;
+      }
       uint16_t* dst = P.qs + row * 256;
       const float x = __uint_as_float(static_cast<uint32_t>(x16[i]) << 16);
       const float y = __uint_as_float(static_cast<uint32_t>(y16[i]) << 16);
@@ -249,9 +253,11 @@ struct Unit {
   long long row0;      // first prepared row of (KV head, sequence)
 };
 
-// The units of this CTA, in order: a run of them (QS = 1, one query tile to a sequence and one split), or every
-// gridDim-th.  Every role has its own walk in its loop, so the run's step is kept to a few instructions: the
-// roles' loops together have to fit the SM's instruction cache.
+// The units of this CTA, in order.  QS = 1 (one query tile to a sequence, one split): CTA c takes KV head c % hkv
+// and the (c / hkv)-th run of its key tiles, so that hkv CTAs read the same cache rows, which lie side by side, at
+// about the same time (DRAM sees 384 hkv bytes in a row).  QS = 2: every gridDim-th unit.  Every role has its
+// own walk in its loop, so the run's step is kept to a few instructions: the roles' loops together have to fit
+// the SM's instruction cache.
 template <int QS>
 struct Walker {
   long long u, left;
@@ -260,9 +266,12 @@ struct Walker {
   Seq s;
   __device__ __forceinline__ explicit Walker(const Params& P) {
     const long long total = P.units[P.num_seqs];
-    if (QS == 1) {
-      u = total * blockIdx.x / gridDim.x;
-      left = total * (blockIdx.x + 1) / gridDim.x - u;
+    if (QS == 1) {  // the grid is a multiple of hkv
+      const int runs = static_cast<int>(gridDim.x) / P.hkv, run = static_cast<int>(blockIdx.x) / P.hkv;
+      const long long tiles = total / P.hkv;
+      u = tiles * run / runs;
+      left = tiles * (run + 1) / runs - u;
+      u *= P.hkv;
     } else {
       u = blockIdx.x;
       left = u < total ? (total - u + gridDim.x - 1) / gridDim.x : 0;
@@ -279,9 +288,8 @@ struct Walker {
     b = a;
     if (QS == 1) {
       load_seq(P, b, s);
-      const int r = static_cast<int>(u - P.units[b]);
-      g = r / s.tiles;
-      kt = r - g * s.tiles;
+      kt = static_cast<int>((u - P.units[b]) / P.hkv);
+      g = static_cast<int>(blockIdx.x) % P.hkv;
     } else {
       --b;  // entered by the first step
     }
@@ -290,10 +298,9 @@ struct Walker {
     if (left == 0) return false;
     --left;
     if (QS == 1) {
-      while (g == P.hkv) {  // the next sequence that has units
+      while (kt == s.tiles) {  // the next sequence that has tiles
         load_seq(P, ++b, s);
         kt = 0;
-        g = s.tiles > 0 ? 0 : P.hkv;
       }
     } else {
       while (u >= hi) {
@@ -321,10 +328,7 @@ struct Walker {
     w.qt0 = 0;
     w.qt1 = 1;
     if (QS == 1) {
-      if (++kt == s.tiles) {
-        kt = 0;
-        ++g;
-      }
+      ++kt;
     } else {
       w.qt0 = static_cast<int>(static_cast<long long>(nq) * f / P.splits);
       w.qt1 = static_cast<int>(static_cast<long long>(nq) * (f + 1) / P.splits);
@@ -370,17 +374,14 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
   Walker<QS> walk(P);
   Unit w;
   bool bad = false, more = true;
-  int row[3], g[3];  // of the unit to copy, and the next two
+  int row[3], g[3], n[3];  // of the unit to copy, and the next two
   auto load = [&](int i) {
-    row[i] = -1;
     g[i] = -1;
     if (more) more = walk.next_busy(P, w);
     if (!more) return;
     g[i] = w.g;
-    if (row0 + lane < w.nk) {
-      row[i] = __ldg(P.kv_indices + w.kv_beg + w.k0 + row0 + lane);
-      if (row[i] < 0) row[i] = P.cache_rows;  // outside the cache on either side
-    }
+    n[i] = w.nk - row0;
+    row[i] = lane < n[i] ? __ldg(P.kv_indices + w.kv_beg + w.k0 + row0 + lane) : -1;
   };
   uint32_t c = 0;
   auto copy = [&](int i) -> bool {  // false at the end, or when the wait gave up
@@ -389,16 +390,16 @@ __device__ __forceinline__ void role_fetch(uint8_t* smem, Ctrl* C, const Params&
     const bool ok = c < KS || wait(C, &C->k_empty[st], (c / KS - 1) & 1, P.wait_limit_ns);
     if (!__all_sync(0xffffffffu, ok)) return false;
     const uint16_t* from = P.k_cache + g[i] * kHeadDimQK + 8 * l8;
-    uint32_t dst = smem_u32(smem + st * kStage) + static_cast<uint32_t>(row0 + r4) * 128u;
-#pragma unroll 1
-    for (int p = 0; p < 8; ++p, dst += 512) {
+    const uint32_t dst = smem_u32(smem + st * kStage) + static_cast<uint32_t>(row0 + r4) * 128u;
+#pragma unroll 4
+    for (int p = 0; p < 8; ++p) {
       const int k = __shfl_sync(0xffffffffu, row[i], 4 * p + r4);
-      const bool in = k >= 0 && k < P.cache_rows;
-      bad |= k >= P.cache_rows;  // an index outside the cache: zeros, reported
-      const uint16_t* src = in ? from + static_cast<size_t>(k) * stride : P.k_cache;
-      const uint32_t nb = in ? 16u : 0u, at = dst + ((l8 ^ ((4 * p + r4) & 7)) << 4);
+      const bool in = static_cast<uint32_t>(k) < static_cast<uint32_t>(P.cache_rows);
+      bad |= !in && 4 * p + r4 < n[i];  // an index outside the cache: zeros, reported
+      const uint16_t* src = from + static_cast<size_t>(in ? k : 0) * stride;
+      const uint32_t nb = in ? 16u : 0u, at = dst + 512u * p + ((l8 ^ ((4 * p + r4) & 7)) << 4);
 #pragma unroll
-      for (int u = 0; u < 3; ++u) cp_async_16(at + u * kUnit, src + (in ? 64 * u : 0), nb);
+      for (int u = 0; u < 3; ++u) cp_async_16(at + u * kUnit, src + 64 * u, nb);
     }
     cp_async_mbar_arrive_noinc(&C->k_landed[st]);
     ++c;
@@ -609,7 +610,9 @@ __device__ __forceinline__ void role_mma(uint8_t* smem, Ctrl* C, uint32_t tmem, 
   }
 }
 
-// Adds 2^(s sl2 - lse2) over N score columns; masked: of those in [lo, hi) only.
+// Adds 2^(s sl2 - lse2) over N score columns; masked: of those in [lo, hi) only.  (Half of the exponentials as
+// polynomials on the FMA pipe, so that ex2's 16 a cycle are not what two groups at work share, was slower: 96
+// against 90 us for a 300-token chunk.)
 template <int N, bool kMasked>
 __device__ __forceinline__ void add_columns(const uint32_t (&s)[N], const float* lse2, float sl2, int lo, int hi,
                                             float2& a0, float2& a1) {
