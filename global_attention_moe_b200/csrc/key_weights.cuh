@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads) kw_join_kernel(const __grid_cons
   // written, and what is read does not count
   float v = 0.f;
   if (in) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < rows; ++k) v += P.partial[static_cast<size_t>(k) * P.total_kv + i];
   }
   const float p = in && P.prev != nullptr ? P.prev[i] : 0.f;

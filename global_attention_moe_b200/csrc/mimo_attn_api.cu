@@ -759,8 +759,37 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
 }
 
 // ---------------------------------------------------------------- routing
+// The kernel of four threads per token: whole blocks of eight experts to a group, at most eight groups and
+// choices, and tokens for every warp that an SM holds (24 of 8 tokens at 256 experts: from 28416 tokens).
+template <int P, bool kSoftmax>
+bool launch_route_bulk(const rg::RouteParams& R, const rg::FastShape& F, int sms, int dev, cudaStream_t stream) {
+  const bool grouped = R.top_groups < R.groups;
+  const int size = grouped ? R.E / R.groups : R.E;
+  if (R.E > 256 || R.top_k > 8 || size % 8 != 0 || (grouped && R.groups > 8)) return false;
+  constexpr int tokens = rg::kBulkWarps * rg::kBulkTokens;  // of a CTA at a time
+  // rows and biases; the exact paths use a warp's rows for max(E, 32 P) words
+  const size_t smem = ((size_t)tokens * (R.E + rg::kBulkPad) + R.E) * 4;
+  if (rg::kBulkTokens * (R.E + rg::kBulkPad) < 32 * P) return false;
+  const int per_sm = (int)std::min<size_t>(6, (size_t)220 * 1024 / (smem + 1024));
+  const long long ctas = (R.T + tokens - 1) / tokens;
+  if (ctas < (long long)per_sm * sms) return false;  // the warp kernel spreads fewer tokens wider
+  static std::atomic<int> state[64];  // 0 unknown, 1 ready, -1 failed
+  if (dev < 0 || dev >= 64) return false;
+  if (state[dev].load() == 0)
+    state[dev].store(cudaFuncSetAttribute(rg::route_bulk_kernel<P, kSoftmax>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          96 * 1024) == cudaSuccess
+                         ? 1
+                         : -1);
+  if (state[dev].load() != 1) return false;
+  rg::route_bulk_kernel<P, kSoftmax><<<(unsigned)(per_sm * sms), rg::kBulkThreads, smem, stream>>>(R, F);
+  return true;
+}
+
 template <int P>
-void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, cudaStream_t stream) {
+void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigned grid, int sms, int dev,
+                       cudaStream_t stream) {
+  if (R.softmax ? launch_route_bulk<P, true>(R, F, sms, dev, stream) : launch_route_bulk<P, false>(R, F, sms, dev, stream))
+    return;
   const size_t smem = (size_t)rg::kWarps * std::max(R.E, 32 * P) * 4;
   const bool full = F.P == P && F.S == (F.P << F.lg) && (R.groups << F.lg) == 32;
   if (R.softmax) {
@@ -776,17 +805,17 @@ void launch_route_fast(const rg::RouteParams& R, const rg::FastShape& F, unsigne
   }
 }
 
-void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, cudaStream_t stream) {
+void launch_route(const rg::RouteParams& R, unsigned grid, size_t smem, int sms, int dev, cudaStream_t stream) {
   rg::FastShape F;
   F.S = R.E / R.groups;
   F.lg = 5;
   while ((R.groups << F.lg) > 32) --F.lg;
   F.P = (F.S + (1 << F.lg) - 1) >> F.lg;
-  if (F.P <= 1) launch_route_fast<1>(R, F, grid, stream);
-  else if (F.P <= 2) launch_route_fast<2>(R, F, grid, stream);
-  else if (F.P <= 4) launch_route_fast<4>(R, F, grid, stream);
-  else if (F.P <= 8) launch_route_fast<8>(R, F, grid, stream);
-  else if (F.P <= 16) launch_route_fast<16>(R, F, grid, stream);
+  if (F.P <= 1) launch_route_fast<1>(R, F, grid, sms, dev, stream);
+  else if (F.P <= 2) launch_route_fast<2>(R, F, grid, sms, dev, stream);
+  else if (F.P <= 4) launch_route_fast<4>(R, F, grid, sms, dev, stream);
+  else if (F.P <= 8) launch_route_fast<8>(R, F, grid, sms, dev, stream);
+  else if (F.P <= 16) launch_route_fast<16>(R, F, grid, sms, dev, stream);
   else rg::route_grouped_kernel<<<grid, rg::kThreads, smem, stream>>>(R);  // e.g. 17 groups of 30
 }
 
@@ -1316,7 +1345,7 @@ int mimo_moe_route_grouped(const float* logits, const float* bias, int64_t token
   P.scale = scale;
   const unsigned grid = (unsigned)std::min<long long>((tokens + rg::kWarps - 1) / rg::kWarps, 16LL * info->sms);
   const size_t smem = (size_t)rg::kWarps * num_experts * 4;
-  launch_route(P, grid, smem, static_cast<cudaStream_t>(stream));
+  launch_route(P, grid, smem, info->sms, dev, static_cast<cudaStream_t>(stream));
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 

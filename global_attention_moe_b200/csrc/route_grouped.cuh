@@ -28,6 +28,7 @@
 
 #include <stdint.h>
 
+#include "cp_async.cuh"
 #include "neighbors.cuh"
 
 namespace mimo {
@@ -208,9 +209,8 @@ __device__ __forceinline__ void sort_desc(int (&k)[N]) {
           }
 }
 
-__device__ __forceinline__ float as_float(int k) { return __uint_as_float(static_cast<uint32_t>(k)); }
-
-constexpr int kNone = static_cast<int>(0x80000000u);  // below every key (as a float -0)
+constexpr int kNone = static_cast<int>(0x80000000u);  // below every key
+__device__ __forceinline__ float as_float(int k) { return __uint_as_float(static_cast<uint32_t>(k)); }  // kNone: -0
 constexpr int kInf = 0x7F800000;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -243,7 +243,8 @@ struct Lane {
     float high = 0.f;
 #pragma unroll
     for (int m = 0; m < P; ++m) {
-      bias[m] -= low;
+      // finite, so that the place in the low bits of a key does not make a NaN of -inf
+      bias[m] = bias[m] - low < -1e30f ? -1e30f : bias[m] - low;
       high = fmaxf(high, bias[m]);
     }
     most = warp_max(high) + fabsf(low);
@@ -309,7 +310,8 @@ struct Lane {
 template <int P>
 __device__ __forceinline__ bool choose_groups(const RouteParams& R, const FastShape& F, const int (&key)[P], int g,
                                               float margin, bool& kept) {
-  float a = as_float(key[0]), b = P > 1 ? as_float(key[P > 1 ? 1 : 0]) : -0.f;
+  auto or_none = [](int k) { return k == kNone ? -INFINITY : as_float(k); };
+  float a = or_none(key[0]), b = P > 1 ? or_none(key[P > 1 ? 1 : 0]) : -INFINITY;
 #pragma unroll 1
   for (int o = 1; o < (1 << F.lg); o <<= 1) {
     const float a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
@@ -480,6 +482,270 @@ __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) route_fast_kernel(co
       if (!route_candidates<P, kSoftmax>(R, F, tok, lane, reinterpret_cast<int*>(s_key))) {
         __syncwarp();
         route_exact_call(R, tok, lane, s_key);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many tokens: four threads per token
+// The warp kernel spends most of its instructions on exchanges between lanes.  With enough tokens to fill the
+// GPU with eight to a warp, four threads take a token: rows come into shared memory (cp.async), keys become
+// integers of 23 bits above 8 bits of 255 - expert, and every choice is minimum and maximum of integers:
+//   1. keys, kept in place, and each group's two largest (a group's blocks of eight experts go round the four);
+//   2. the groups by their sums;
+//   3. the kept groups' keys in blocks of eight: sorted, then merged into the thread's sorted eight largest, at
+//      the end into the token's; the largest of what falls out is kept too, so that the k-th and the next can
+//      be compared.
+// Errors, and what is left for the exact paths, as in the warp kernel, with the keys' spacing 2^-23 of their
+// range.  One thread per token takes fewer instructions (226 a token against 474 of the warp kernel at 256
+// experts in 8 groups), but 32 rows to a warp leave six warps to an SM, and it was slower than the warp kernel
+// (185 against 160 us for 262144 tokens).
+constexpr int kBulkWarps = 4;  // per CTA
+constexpr int kBulkThreads = 32 * kBulkWarps;
+constexpr int kBulkH = 4;                // threads to a token
+constexpr int kBulkTokens = 32 / kBulkH;  // tokens to a warp
+constexpr int kBulkPad = 4;              // floats: rows 16 bytes apart in the banks
+constexpr float kBulkOne = 8388608.f;    // 2^23: adds an integer into the low bits
+
+__device__ __forceinline__ int max3(int a, int b, int c) { return max(a, max(b, c)); }
+
+// The eight largest of two descending lists of eight, descending, and the largest of the rest.
+__device__ __forceinline__ void merge8(int (&r)[8], const int (&k)[8], int& rest) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int a = r[i], b = k[7 - i];
+    r[i] = max(a, b);
+    rest = max(rest, min(a, b));
+  }
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)  // r is bitonic
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const int a = r[i], b = r[i + d];
+        r[i] = max(a, b);
+        r[i + d] = min(a, b);
+      }
+}
+
+template <int P, bool kSoftmax>
+__global__ void __launch_bounds__(kBulkThreads) route_bulk_kernel(const __grid_constant__ RouteParams R,
+                                                                  const __grid_constant__ FastShape F) {
+  extern __shared__ __align__(16) float sm[];  // per warp 8 rows of E + 4; then E biases
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, stride = R.E + kBulkPad;
+  const int own = lane / kBulkH, h = lane % kBulkH;
+  float* rows = sm + warp * kBulkTokens * stride;
+  float* mine = rows + own * stride;
+  float* s_bias = sm + kBulkWarps * kBulkTokens * stride;
+  // biases moved up by the least of them (those far below all others aside: -inf, a negative key)
+  float low = 0.f, high = 0.f;
+  if (R.bias != nullptr) {
+    low = INFINITY;
+    high = -INFINITY;
+    for (int e = lane; e < R.E; e += 32) {
+      const float b = __ldg(R.bias + e);
+      if (b > -1024.f) low = fminf(low, b);
+      high = fmaxf(high, b == b ? b : INFINITY);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    high = warp_max(high);
+  }
+  const bool plain = high - low < 1024.f && fabsf(low) < 1024.f;  // else every token is left for the exact paths
+  const float range = plain ? high - low : 1.f, off = plain ? fabsf(low) : 0.f;
+  for (int e = threadIdx.x; e < R.E; e += kBulkThreads) {
+    const float b = R.bias != nullptr ? __ldg(R.bias + e) : 0.f;
+    s_bias[e] = b >= low ? b - low : -INFINITY;
+  }
+  __syncthreads();
+  const int groups = R.top_groups < R.groups ? R.groups : 1, S = R.E / groups;
+  const int64_t tiles = (R.T + kBulkTokens - 1) / kBulkTokens, step = static_cast<int64_t>(gridDim.x) * kBulkWarps;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kBulkWarps + warp;
+  const int chunks = R.E / 4;
+#pragma unroll 1
+  for (int64_t tile = first; tile < tiles; tile += step) {
+    const int64_t t0 = tile * kBulkTokens, tok = t0 + own;
+    const int live = static_cast<int>(min(static_cast<int64_t>(kBulkTokens), R.T - t0));
+    const float* from = R.logits + t0 * R.E;
+    for (int r = 0; r < live; ++r, from += R.E)
+      for (int c = lane; c < chunks; c += 32) cp_async_16(smem_u32(rows + r * stride + 4 * c), from + 4 * c, 16u);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncwarp();
+    float mx = 0.f, inv = 1.f;
+    if (kSoftmax) {
+      mx = -INFINITY;
+      for (int e = 4 * h; e < R.E; e += 4 * kBulkH) {
+        const float4 v = *reinterpret_cast<const float4*>(mine + e);
+        mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+      }
+#pragma unroll
+      for (int o = 1; o < kBulkH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      float sum = 0.f;
+      for (int e = 4 * h; e < R.E; e += 4 * kBulkH) {
+        const float4 v = *reinterpret_cast<const float4*>(mine + e);
+        sum += (ex2_approx((v.x - mx) * kLog2e) + ex2_approx((v.y - mx) * kLog2e)) +
+               (ex2_approx((v.z - mx) * kLog2e) + ex2_approx((v.w - mx) * kLog2e));
+      }
+#pragma unroll
+      for (int o = 1; o < kBulkH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      inv = rcp_approx(sum);
+      __syncwarp();  // the row is rewritten below
+    }
+    // keys as integers: 2^23 - 2048 for the largest possible score and bias
+    const float scale = (kBulkOne - 2048.f) / ((kSoftmax ? inv : 1.f) + range);
+    // twice a key's error, in steps: the sigmoid's 2^-21 or the softmax's 2^-18 of the score (Lane::keys), the
+    // roundings of the bias's move and of the sum
+    const float err = scale * ((kSoftmax ? 0x1p-17f * inv : 0x1p-20f) + 0x1p-22f * (range + off)) + 6.f;
+    const int margin = static_cast<int>(err) + 1;
+    bool sure = plain && (!kSoftmax || (inv > 0.f && inv <= 1.5f));
+    int v[8];  // the groups: the sum of the two largest (24 bits), the lower group ahead; a negative key: none
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      v[g] = kNone;
+      if (g >= groups) continue;
+      int a = kNone, b = kNone;  // the group's two largest
+#pragma unroll 1
+      for (int e = g * S + 8 * h; e < (g + 1) * S; e += 8 * kBulkH) {
+        int k[8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float4 v4 = *reinterpret_cast<const float4*>(mine + e + 4 * u);
+          const float4 w4 = *reinterpret_cast<const float4*>(s_bias + e + 4 * u);
+          const float x[4] = {v4.x, v4.y, v4.z, v4.w}, bias[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float s = kSoftmax ? ex2_approx((x[i] - mx) * kLog2e) * inv : rcp_approx(1.f + ex2_approx(x[i] * -kLog2e));
+            const uint32_t q = __float_as_uint(fmaf(s + bias[i], scale, kBulkOne));
+            k[4 * u + i] = static_cast<int>(q * 256u + static_cast<uint32_t>(255 - (e + 4 * u + i)));
+          }
+          *reinterpret_cast<int4*>(mine + e + 4 * u) = make_int4(k[4 * u], k[4 * u + 1], k[4 * u + 2], k[4 * u + 3]);
+        }
+        if (groups > 1) {
+          int p[4], q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = max(k[2 * i], k[2 * i + 1]);
+            q[i] = min(k[2 * i], k[2 * i + 1]);
+          }
+#pragma unroll
+          for (int d = 2; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < d; ++i) {
+              q[i] = max3(min(p[i], p[i + d]), q[i], q[i + d]);
+              p[i] = max(p[i], p[i + d]);
+            }
+          b = max3(min(a, p[0]), b, q[0]);
+          a = max(a, p[0]);
+        }
+      }
+      if (groups > 1) {
+#pragma unroll
+        for (int o = 1; o < kBulkH; o <<= 1) {
+          const int a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+          b = max3(min(a, a2), b, b2);
+          a = max(a, a2);
+        }
+        v[g] = b < 0 ? kNone : (((a >> 8) + (b >> 8)) << 3) | (7 - g);
+      }
+    }
+    uint32_t kept = 1u;
+    if (groups > 1) {
+      kept = 0;
+      int least = 0x7FFFFFFF, most = 0;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        int rank = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rank += v[j] > v[g] ? 1 : 0;
+        const bool in = g < groups && rank < R.top_groups;
+        kept |= in ? 1u << g : 0u;
+        least = min(least, in ? v[g] : 0x7FFFFFFF);
+        most = max(most, in ? 0 : v[g]);
+      }
+      sure = sure && least >= 0 && __popc(kept) == R.top_groups && (least >> 3) - (most >> 3) > 2 * margin;
+    }
+    int r[8], rest = kNone;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = kNone;
+    for (int j = 0; j < (groups > 1 ? R.top_groups : 1); ++j) {
+      // the token's j-th kept group (where there are fewer, the token is left anyway)
+      const int g = kept ? __ffs(kept) - 1 : 0;
+      kept &= kept - 1;
+#pragma unroll 1
+      for (int e = g * S + 8 * h; e < (g + 1) * S; e += 8 * kBulkH) {
+        const int4 u = *reinterpret_cast<const int4*>(mine + e), w = *reinterpret_cast<const int4*>(mine + e + 4);
+        int k[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+        sort_desc<8>(k);
+        merge8(r, k, rest);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kBulkH; o <<= 1) {
+      int k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(0xffffffffu, r[i], o);
+      rest = max(rest, __shfl_xor_sync(0xffffffffu, rest, o));
+      merge8(r, k, rest);
+    }
+    // neighbours that are too near one another, or a key that is none
+    const int64_t gap = static_cast<int64_t>(margin) * 256 + 255;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < R.top_k) {
+        const int next = i < 7 ? r[i < 7 ? i + 1 : 7] : rest;
+        sure = sure && r[i] >= 0 && static_cast<int64_t>(r[i]) - next > gap;
+      }
+    // choices 2 h and 2 h + 1 are this thread's to write
+    int e2[2];
+    float w2[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int key = h == 0 ? r[u] : h == 1 ? r[2 + u] : h == 2 ? r[4 + u] : r[6 + u];
+      e2[u] = 255 - (key & 255);
+      w2[u] = 0.f;
+      if (2 * h + u < R.top_k && sure && tok < R.T) {
+        const float x = __ldg(R.logits + tok * R.E + e2[u]);
+        sure = x - mx > -80.f;  // a score that FP32 holds
+        w2[u] = kSoftmax ? expf(x - mx) * inv : rcp_approx(1.f + expf(-x));
+      }
+    }
+    float total = w2[0] + w2[1];
+    int all = sure ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < kBulkH; o <<= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      all &= __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (tok < R.T) {
+      const float f = R.normalize ? rcp_approx(total) * R.scale : R.scale;
+      int32_t* ids = R.ids + tok * R.top_k;
+      float* out = R.weights + tok * R.top_k;
+      if (!all) {
+        if (h == 0) ids[0] = -1;  // left for below
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (2 * h + u < R.top_k) {
+            ids[2 * h + u] = e2[u];
+            out[2 * h + u] = w2[u] * f;
+          }
+      }
+    }
+    __syncwarp();  // the rows are read
+  }
+  __syncwarp();
+  // the tokens of this warp that were left
+#pragma unroll 1
+  for (int64_t tile = first; tile < tiles; tile += step) {
+    const int64_t t = tile * kBulkTokens + lane;
+    unsigned left = __ballot_sync(0xffffffffu, lane < kBulkTokens && t < R.T && *(R.ids + t * R.top_k) < 0);
+    for (; left; left &= left - 1) {
+      const int64_t tok = tile * kBulkTokens + __ffs(left) - 1;
+      if (!route_candidates<P, kSoftmax>(R, F, tok, lane, reinterpret_cast<int*>(rows))) {
+        __syncwarp();
+        route_exact_call(R, tok, lane, rows);
       }
       __syncwarp();
     }

@@ -81,24 +81,26 @@ def route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, softma
     key = np.where(np.isnan(key), np.float32(-np.inf), key)
     T, E = key.shape
     size = E // num_groups
-    ids = np.empty((T, top_k), dtype=np.int32)
-    w = np.empty((T, top_k))
-    for t in range(T):
-        gs = []
-        for g in range(num_groups):
-            k = sorted((key[t, e] for e in range(g * size, (g + 1) * size)), reverse=True)
-            with np.errstate(all="ignore"):
-                v = np.float32(k[0] + k[1]) if size > 1 else k[0]
-            gs.append(-np.inf if np.isnan(v) else v)
-        kept = sorted(range(num_groups), key=lambda g: (-gs[g], g))[:top_groups]
-        open_ = [e for g in kept for e in range(g * size, (g + 1) * size)]
-        ids[t] = sorted(open_, key=lambda e: (-key[t, e], e))[:top_k]
-        c = s[t, ids[t]]
-        if normalize:
-            total = c.sum()
-            c = np.zeros_like(c) if total == 0 else c / total
-        w[t] = scale * c
-    return ids, w
+    if num_groups > 1:
+        by = np.sort(key.reshape(T, num_groups, size), -1)
+        with np.errstate(all="ignore"):
+            gs = (by[..., -1] + by[..., -2]).astype(np.float32) if size > 1 else by[..., -1]
+        gs = np.where(np.isnan(gs), np.float32(-np.inf), gs)
+        kept = np.argsort(-gs, axis=-1, kind="stable")[:, :top_groups]  # stable: ties to the lower group
+        open_ = np.zeros((T, num_groups), dtype=bool)
+        np.put_along_axis(open_, kept, True, -1)
+        open_ = np.repeat(open_, size, -1)
+    else:
+        open_ = np.ones((T, E), dtype=bool)
+    # experts of the kept groups first, then by key, then by index
+    order = np.lexsort((np.broadcast_to(np.arange(E), (T, E)), -key.astype(np.float64), ~open_), axis=-1)
+    ids = order[:, :top_k].astype(np.int32)
+    w = np.take_along_axis(s, ids.astype(np.int64), -1)
+    if normalize:
+        total = w.sum(-1, keepdims=True)
+        with np.errstate(all="ignore"):
+            w = np.where(total == 0, 0.0, w / total)
+    return ids, scale * w
 
 
 def route_bwd(logits, ids, dweights, softmax=False, normalize=True, scale=1.0):

@@ -260,6 +260,15 @@ CASES = {
                                for kind in ("ties", "near", "flat", "far", "masked")
                                for E, groups, top, softmax, bias in ((256, 8, 4, False, True), (256, 1, 1, True, False),
                                                                      (128, 4, 2, False, False), (160, 1, 1, True, True))],
+    # enough tokens for the kernel of one thread per token on an SM or two (and a ragged last tile)
+    "route_many": lambda be: [check_route(be, T, E, k, groups, top, softmax, normalize, bias, 75 + E, kind, 2.5)
+                              for T, E, k, groups, top, softmax, normalize, bias, kind in (
+                                  (1111, 256, 8, 8, 4, False, True, True, "normal"), (1050, 256, 8, 1, 1, True, True, False, "normal"),
+                                  (1333, 64, 6, 4, 1, True, False, True, "normal"), (1100, 128, 3, 8, 8, False, True, False, "normal"),
+                                  (1100, 160, 8, 4, 2, False, True, True, "normal"), (1200, 72, 1, 3, 2, True, True, False, "normal"),
+                                  (1100, 16, 8, 2, 1, False, True, True, "normal"), (1100, 256, 8, 8, 4, False, True, True, "ties"),
+                                  (1100, 64, 8, 8, 4, True, True, False, "near"), (1100, 64, 8, 1, 1, False, True, False, "far"),
+                                  (1100, 128, 8, 4, 2, True, True, False, "masked"), (1100, 64, 4, 8, 2, False, True, True, "flat"))],
     "route_values": lambda be: route_values(be),
     "route_bwd": lambda be: [check_route_bwd(be, *c) for c in (
         (5, 256, 8, False, True, 80), (5, 256, 8, True, True, 81), (5, 128, 6, True, False, 82, 2.5),
@@ -317,13 +326,13 @@ def norm_values(be):
 
 def route_values(be):
     """NaN and infinite logits and biases: ids stay distinct experts, and the rest of the batch is not touched."""
-    for softmax in (False, True):
-        x = route_logits(6, 64, 3)
+    for softmax, T in ((False, 6), (True, 6), (False, 2100), (True, 2100)):
+        x = route_logits(T, 64, 3)
         x[1, 5] = np.nan
         x[2] = np.nan
         x[3, 9] = -np.inf
         x[4] = -np.inf
-        clean = [0, 3, 5]
+        clean = [0, 3, *range(5, T)]
         ids, w = be.route(x, None, 8, 8, 4, softmax, True, 1.0)
         with np.errstate(all="ignore"):
             rid, rw = steps.route_grouped(x, None, 8, 8, 4, softmax, True, 1.0)
@@ -334,11 +343,19 @@ def route_values(be):
             assert np.all(w[4] == 0)  # every score is zero
     b = np.zeros(64, dtype=np.float32)
     b[3], b[4], b[17] = np.nan, -np.inf, np.inf
-    x = route_logits(3, 64, 4)
-    ids, w = be.route(x, b, 8, 4, 2, False, True, 1.0)
-    rid, rw = steps.route_grouped(x, b, 8, 4, 2, False, True, 1.0)
-    assert np.array_equal(ids, rid) and np.all(ids[:, 0] == 17)
-    close(w, rw, np.abs(rw) * 2.0 ** -20, "weights")
+    off = (0.1 * np.random.default_rng(5).standard_normal(64)).astype(np.float32)
+    off[::3] = -1e9  # experts switched off by their bias
+    off[::7] = -np.inf
+    for T in (3, 2100):
+        x = route_logits(T, 64, 4)
+        ids, w = be.route(x, b, 8, 4, 2, False, True, 1.0)
+        rid, rw = steps.route_grouped(x, b, 8, 4, 2, False, True, 1.0)
+        assert np.array_equal(ids, rid) and np.all(ids[:, 0] == 17)
+        close(w, rw, np.abs(rw) * 2.0 ** -20, "weights")
+        ids, w = be.route(x, off, 8, 4, 2, False, True, 1.0)
+        rid, rw = steps.route_grouped(x, off, 8, 4, 2, False, True, 1.0)
+        assert np.array_equal(ids, rid)
+        close(w, rw, np.abs(rw) * 2.0 ** -20, "weights")
 
 
 def route_bwd_places(be):

@@ -121,6 +121,14 @@ def test_route_sizes(be, T, E, k, groups, top, softmax, bias):
     S.check_route(be, T // 3, E, k, groups, top, softmax, True, bias, T + E + 1, "near")
 
 
+@pytest.mark.parametrize("T,E,k,groups,top,softmax,bias,kind", [
+    (40001, 256, 8, 8, 4, False, True, "normal"), (30011, 256, 8, 1, 1, True, False, "normal"),
+    (60000, 128, 6, 4, 2, True, True, "normal"), (80001, 64, 8, 8, 4, False, True, "ties"),
+    (30000, 256, 8, 8, 4, False, True, "near"), (50000, 160, 6, 4, 3, False, False, "masked")])
+def test_route_many_tokens(be, T, E, k, groups, top, softmax, bias, kind):
+    S.check_route(be, T, E, k, groups, top, softmax, True, bias, T + E, kind, scale=2.5)
+
+
 @pytest.mark.parametrize("kv,q,hq,hkv,window,sink", [([3000, 1025, 640], [1, 1, 1], 64, 4, -1, False),
                                                      ([2100, 900, 129], [8, 8, 8], 64, 4, -1, False),
                                                      ([1500, 300], [8, 1], 64, 8, 128, True),
@@ -217,7 +225,7 @@ def calls(M):
     g = torch.Generator(device="cuda").manual_seed(5)
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
     x, r, w = rnd(700, 1024).bfloat16(), rnd(700, 1024).bfloat16(), rnd(1024)
-    logits, bias = rnd(900, 256), rnd(256)
+    logits, bias, many = rnd(900, 256), rnd(256), rnd(33000, 256)
     ids = torch.argsort(rnd(900, 256), -1)[:, :8].to(torch.int32).contiguous()
     dw = rnd(900, 8)
     lens = [700, 300]
@@ -234,6 +242,7 @@ def calls(M):
         ("rms_norm_fp8", lambda s: M.rms_norm_fp8(x, w, r, with_bf16=True, stream=s)),
         ("rms_norm_bwd", lambda s: M.rms_norm_bwd(x, w, r, x, stream=s)),
         ("moe_route_grouped", lambda s: M.moe_route_grouped(logits, bias, 8, 8, 4, stream=s)),
+        ("moe_route_many", lambda s: M.moe_route_grouped(many, bias, 8, 8, 4, stream=s)),
         ("moe_route_softmax", lambda s: M.moe_route_grouped(logits, None, 8, score=M.ROUTE_SOFTMAX, stream=s)),
         ("moe_route_bwd", lambda s: (M.moe_route_bwd(logits, ids, dw, stream=s),)),
         ("key_weights", lambda s: (M.decode_key_weights(q, kc, idx, ptr, cu, lse, 3, 700, M.LAYER_GLOBAL, -1, 1e7, stream=s),)),
