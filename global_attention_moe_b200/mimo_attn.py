@@ -585,6 +585,8 @@ def kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first=0, k
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first, keep_recent)
+    # no sequence is longer than an int32, and what does not fit one is not to wrap
+    budget, keep_first, keep_recent = (max(-1, min(n, 0x7FFFFFFF)) for n in (budget, keep_first, keep_recent))
     idx, freed = torch.empty_like(kv_indices), torch.empty_like(kv_indices)
     w, ptr = torch.empty_like(weights), torch.empty_like(kv_indptr)
     st = LIB.mimo_kv_evict(weights.data_ptr(), kv_indices.data_ptr(), kv_indptr.data_ptr(), B1 - 1, total, max_kv_len,

@@ -465,7 +465,7 @@ MIMO_API int mimo_moe_route_grouped(const float* logits, const float* bias, int6
  * (the choice itself and the bias have none): dlogits fp32 [T, E], every element
  * written.  dweights fp32 [T, top_k].  An id outside [0, E) is an empty place and
  * takes no part; the same id twice adds up.  Limits and alignment as above, and
- * dlogits 16-byte aligned.  Does not synchronise.
+ * dlogits 16-byte aligned and no input's memory.  Does not synchronise.
  */
 MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const float* dweights, int64_t tokens,
                                 int num_experts, int top_k, int score, int normalize, float scale, float* dlogits,

@@ -350,6 +350,13 @@ def test_empty_calls(M):
     z = torch.zeros(3, dtype=torch.int32, device="cuda")
     idx, w, ptr, freed = M.kv_evict(e(0), e(0, dtype=torch.int32), z, 0, 5)
     assert torch.equal(ptr, z)
+    # a budget beyond any length keeps everything
+    a, b = torch.rand(6, device="cuda"), torch.arange(6, dtype=torch.int32, device="cuda")
+    idx, w, ptr, freed = M.kv_evict(a, b, torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda"), 4, 10 ** 12)
+    assert torch.equal(idx, b) and torch.equal(w, a) and ptr.tolist() == [0, 2, 6]
+    for counts in ((-10 ** 12,), (2, 2 ** 32 + 1), (2, 0, 2 ** 32), (2, -2 ** 32)):  # refused, not wrapped
+        with pytest.raises(M.MimoAttnError):
+            M.kv_evict(a, b, torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda"), 4, *counts)
     # no new queries: what was accumulated so far
     i = torch.arange(10, dtype=torch.int32, device="cuda")
     ptr = torch.tensor([0, 4, 10], dtype=torch.int32, device="cuda")
