@@ -213,6 +213,10 @@ constexpr int kNone = static_cast<int>(0x80000000u);  // below every key
 __device__ __forceinline__ float as_float(int k) { return __uint_as_float(static_cast<uint32_t>(k)); }  // kNone: -0
 constexpr int kInf = 0x7F800000;
 constexpr float kLog2e = 1.4426950408889634f;
+// Negative keys (biases at most kFarBias, -1024) count as none, and a group whose second key is one as below all
+// others.  With high the largest moved bias and low the move, its sum is at most high + 1 and kFarBias - low + 1,
+// which is negative, as that says, while high + |low| is below this.
+constexpr float kMaxSpread = 1000.f, kFarBias = -1024.f;
 
 // A lane's experts (e0 .. e0 + count - 1, count <= P) and their biases, moved up by the least of them (those
 // far below all others aside) so that keys are positive; `most` bounds the moved biases' size and the move.
@@ -235,7 +239,7 @@ struct Lane {
     for (int m = 0; m < P; ++m)
       if (m < count) {
         bias[m] = __ldg(R.bias + e0 + m);
-        if (bias[m] > -1024.f) low = fminf(low, bias[m]);
+        if (bias[m] > kFarBias) low = fminf(low, bias[m]);
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
@@ -248,6 +252,7 @@ struct Lane {
       high = fmaxf(high, bias[m]);
     }
     most = warp_max(high) + fabsf(low);
+    if (!(most < kMaxSpread)) most = INFINITY;  // no bound: every token takes the exact path
   }
   template <bool kFull>
   __device__ __forceinline__ void load(const RouteParams& R, int64_t tok, float (&x)[P]) const {
@@ -343,7 +348,7 @@ __device__ __noinline__ bool route_candidates(const RouteParams& R, const FastSh
   int key[P];
   mine.template load<false>(R, tok, v);
   const float margin = mine.template keys<kSoftmax, false>(v, key, mx, inv);
-  if (__any_sync(0xffffffffu, key[0] >= kInf)) return false;
+  if (!(mine.most < kMaxSpread) || __any_sync(0xffffffffu, key[0] >= kInf)) return false;
   bool kept = true;
   if (R.top_groups < R.groups && !choose_groups<P>(R, F, key, mine.g, margin, kept)) return false;
 #pragma unroll
@@ -545,14 +550,14 @@ __global__ void __launch_bounds__(kBulkThreads) route_bulk_kernel(const __grid_c
     high = -INFINITY;
     for (int e = lane; e < R.E; e += 32) {
       const float b = __ldg(R.bias + e);
-      if (b > -1024.f) low = fminf(low, b);
+      if (b > kFarBias) low = fminf(low, b);
       high = fmaxf(high, b == b ? b : INFINITY);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     high = warp_max(high);
   }
-  const bool plain = high - low < 1024.f && fabsf(low) < 1024.f;  // else every token is left for the exact paths
+  const bool plain = high - low + fabsf(low) < kMaxSpread;  // else every token is left for the exact paths
   const float range = plain ? high - low : 1.f, off = plain ? fabsf(low) : 0.f;
   for (int e = threadIdx.x; e < R.E; e += kBulkThreads) {
     const float b = R.bias != nullptr ? __ldg(R.bias + e) : 0.f;

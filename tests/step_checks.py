@@ -270,6 +270,7 @@ CASES = {
                                   (1100, 64, 8, 8, 4, True, True, False, "near"), (1100, 64, 8, 1, 1, False, True, False, "far"),
                                   (1100, 128, 8, 4, 2, True, True, False, "masked"), (1100, 64, 4, 8, 2, False, True, True, "flat"))],
     "route_values": lambda be: route_values(be),
+    "route_far": lambda be: route_far(be, (3, 2100)),
     "route_bwd": lambda be: [check_route_bwd(be, *c) for c in (
         (5, 256, 8, False, True, 80), (5, 256, 8, True, True, 81), (5, 128, 6, True, False, 82, 2.5),
         (4, 64, 4, False, False, 83, 0.5), (3, 60, 60 // 2, True, True, 84), (2, 512, 32, False, True, 85),
@@ -356,6 +357,26 @@ def route_values(be):
         rid, rw = steps.route_grouped(x, off, 8, 4, 2, False, True, 1.0)
         assert np.array_equal(ids, rid)
         close(w, rw, np.abs(rw) * 2.0 ** -20, "weights")
+
+
+def route_far(be, tokens):
+    """Biases far apart: a group whose largest makes up for a second key far below all other groups' keys."""
+    for T in tokens:
+        for softmax in (False, True):
+            for E in (64, 256):
+                size = E // 8
+                plain, deep = np.zeros(E, dtype=np.float32), np.full(E, -1000.0, dtype=np.float32)
+                plain[:size] = -5000.0
+                plain[0], plain[1], plain[2] = 1500.0, -1030.0, -np.inf
+                deep[size:2 * size] = -1025.0
+                deep[size] = 20.0
+                x = route_logits(T, E, 6)
+                for b, first in ((plain, 0), (deep, size)):
+                    ids, w = be.route(x, b, 8, 8, 2, softmax, True, 1.0)
+                    rid, rw = steps.route_grouped(x, b, 8, 8, 2, softmax, True, 1.0)
+                    assert np.all(rid[:, 0] == first)
+                    assert np.array_equal(ids, rid), f"{T} tokens, {E} experts, softmax {softmax}, group of {first}"
+                    close(w, rw, np.abs(rw) * 2.0 ** -20, "weights")
 
 
 def route_bwd_places(be):

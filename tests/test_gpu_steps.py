@@ -129,6 +129,10 @@ def test_route_many_tokens(be, T, E, k, groups, top, softmax, bias, kind):
     S.check_route(be, T, E, k, groups, top, softmax, True, bias, T + E, kind, scale=2.5)
 
 
+def test_route_biases_far_apart(be):
+    S.route_far(be, (3, 30000))  # the kernels of few and of many tokens
+
+
 @pytest.mark.parametrize("kv,q,hq,hkv,window,sink", [([3000, 1025, 640], [1, 1, 1], 64, 4, -1, False),
                                                      ([2100, 900, 129], [8, 8, 8], 64, 4, -1, False),
                                                      ([1500, 300], [8, 1], 64, 8, 128, True),

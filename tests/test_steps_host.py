@@ -46,10 +46,10 @@ def test_kernels_match_their_definitions(host_library, name):
 
 def test_with_few_sms(host_library):
     """On 1 and 3 SMs every CTA of the persistent kernels walks many rows, tokens and key tiles in turn, and the
-    router takes its kernel of one thread per token."""
+    router takes its kernel of four threads per token."""
     for sms in (1, 3):
-        rc, log = run(host_library, ["norm_bwd", "route", "route_many", "route_values", "route_bwd", "weights_step", "weights_window",
-                              "weights_chunk"], sms)
+        rc, log = run(host_library, ["norm_bwd", "route", "route_many", "route_values", "route_far", "route_bwd", "weights_step",
+                              "weights_window", "weights_chunk"], sms)
         assert rc == 0, log
 
 
