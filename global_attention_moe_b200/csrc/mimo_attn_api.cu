@@ -758,6 +758,10 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
     rms::rms_norm_bwd_kernel<TPR, V, uint16_t><<<grid, rms::kBwdThreads, smem, stream>>>(P);
 }
 
+// An index list's entries for the key weights and the eviction, whose kernels count in int and step up to 256
+// entries past an end.
+constexpr int kMaxListEntries = 0x7FFFF000;
+
 // ---------------------------------------------------------------- routing
 // The kernel of four threads per token: whole blocks of eight experts to a group, at most eight groups and
 // choices, and tokens for every warp that an SM holds (24 of 8 tokens at 256 experts: from 28416 tokens).
@@ -1399,6 +1403,7 @@ int mimo_decode_key_weights(const void* q, const void* k_cache, const int32_t* k
                            rope_dims, 1.f, none, lse);
   if (st != MIMO_OK) return st;
   if ((int64_t)dims->total_q * dims->num_q_heads > INT32_MAX) return MIMO_ERR_UNSUPPORTED;  // rows of a tensor map
+  if (dims->total_kv > kMaxListEntries) return MIMO_ERR_UNSUPPORTED;
   if (dims->total_kv == 0) return MIMO_OK;
   if (!out || !workspace || ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(prev)) & 3u) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < key_weights_plan(dims).bytes)
@@ -1413,7 +1418,8 @@ int mimo_kv_evict(const float* weights, const int32_t* kv_indices, const int32_t
   if (num_seqs < 1 || total_kv < 0 || max_kv_len < 0 || max_kv_len > total_kv || keep_first < 0 || keep_recent < 0 ||
       (int64_t)keep_first + keep_recent > budget)
     return MIMO_ERR_INVALID_ARG;
-  if (num_seqs > (1 << 24)) return MIMO_ERR_UNSUPPORTED;  // the grid
+  // every cluster reads all sequences' bounds, which 65536 of them do in some 30 ms
+  if (num_seqs > (1 << 16) || total_kv > kMaxListEntries) return MIMO_ERR_UNSUPPORTED;
   if (!kv_indptr || !new_indptr) return MIMO_ERR_INVALID_ARG;
   if (total_kv > 0 && (!weights || !kv_indices || !new_indices || !new_weights || !freed)) return MIMO_ERR_INVALID_ARG;
   for (const void* p : {(const void*)weights, (const void*)kv_indices, (const void*)kv_indptr,

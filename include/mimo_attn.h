@@ -487,8 +487,10 @@ MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const f
  * zeros and are recorded.
  * workspace: device, 256-byte aligned, at least
  * mimo_decode_key_weights_workspace_size(dims) bytes (0 for invalid dims; about
- * 516 bytes per new token and query head, and 4 per key and KV head); calls that
- * overlap need one each.  Does not synchronise.
+ * 516 bytes per new token and query head, and 4 per key and KV head, up to 32 times
+ * that where a sequence's queries fill several tiles and there are few keys); calls
+ * that overlap need one each.  total_kv at most 2^31 - 4096 (else
+ * MIMO_ERR_UNSUPPORTED).  Does not synchronise.
  */
 MIMO_API size_t mimo_decode_key_weights_workspace_size(const mimo_decode_dims* dims);
 MIMO_API int mimo_decode_key_weights(const void* q, const void* k_cache, const int32_t* kv_indices,
@@ -510,7 +512,8 @@ MIMO_API int mimo_decode_key_weights(const void* q, const void* k_cache, const i
  *   freed       int32 [total_kv]: the cache rows that left, packed; sequence b's
  *               start at kv_indptr[b] - new_indptr[b]
  * Outputs are written up to the new totals only, and may not overlap inputs.
- * 0 <= keep_first, 0 <= keep_recent, keep_first + keep_recent <= budget.  An
+ * 0 <= keep_first, 0 <= keep_recent, keep_first + keep_recent <= budget; at most
+ * 65536 sequences and 2^31 - 4096 entries (else MIMO_ERR_UNSUPPORTED).  An
  * inconsistent kv_indptr is recorded as MIMO_ERR_BAD_SEQLENS and nothing is
  * written.  The positions of the keys that stay move up with them (a key's
  * position is its place in the list).  Does not synchronise.

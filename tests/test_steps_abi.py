@@ -81,6 +81,7 @@ def test_route_bwd(M, args, expect):
     (dict(out=None), 1), (dict(out=FAKE + 2), 1), (dict(prev=FAKE + 2), 1), (dict(ws=None), 1), (dict(ws=FAKE + 16), 1),
     (dict(ws_bytes=100), 1), (dict(idx=None), 1), (dict(ptr=None), 1), (dict(cu=None), 1), (dict(kc=None), 1),
     (dict(max_q_len=70000, total_q=70000, max_kv_len=70000, total_kv=70000, cache_rows=70000, hq=64, hkv=4), 2),
+    (dict(total_kv=2 ** 31 - 1), 2), (dict(total_kv=0x7FFFF001), 2),
     (dict(total_kv=0, max_kv_len=0, max_q_len=0, total_q=0, q=None, lse=None, kc=None, idx=None, out=None, ws=None), 0),
 ])
 def test_key_weights(M, case, expect):
@@ -103,6 +104,7 @@ def test_key_weights(M, case, expect):
     (dict(budget=-1), 1), (dict(budget=3, first=2, recent=2), 1), (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), 1),
     (dict(w=None), 1), (dict(idx=None), 1), (dict(ptr=None), 1), (dict(ni=None), 1), (dict(nw=None), 1), (dict(np_=None), 1),
     (dict(freed=None), 1), (dict(w=FAKE + 2), 1), (dict(freed=FAKE + 1), 1),
+    (dict(total=2 ** 31 - 1), 2), (dict(total=0x7FFFF001), 2), (dict(B=65537), 2),
 ])
 def test_evict(M, args, expect):
     a = dict(w=FAKE, idx=FAKE, ptr=FAKE, B=2, total=20, most=10, budget=5, first=1, recent=1, ni=FAKE, nw=FAKE, np_=FAKE,
