@@ -203,12 +203,21 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       const float scale = fmaxf(__fdiv_rn(a, kFp8Max), 0x1p-126f);  // a block of zeros: the smallest normal scale
-      const float inv = 1.f / scale;
       if (in) {
+        // The quotients, negated: q = y (1 / scale) and one step with the remainder y - q scale, which is exact
+        // (Markstein), so that they are the rounded y / scale.  With BF16 rows and weights 2 of 10000 lie on a midpoint
+        // of two codes, where the reciprocal's rounding would decide.  Negated, so that zeros keep their sign; an
+        // infinite scale takes no step (codes 0, and NaN where y is infinite).  A division for each: 82 us, for those
+        // near a midpoint 79 to 90, this 73 (16384 x 4096).
+        const float ninv = -1.f / scale, sc = scale < INFINITY ? scale : 0.f;
         uint32_t c[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          c[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e] * inv, f[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 4; ++e) {
+          const float2 y2 = make_float2(f[2 * e], f[2 * e + 1]), ninv2 = make_float2(ninv, ninv);
+          float2 q = fmul2(y2, ninv2);
+          q = ffma2(ffma2(q, make_float2(sc, sc), y2), ninv2, q);
+          c[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) ^ 0x8080u;
+        }
         reinterpret_cast<uint2*>(P.codes + row * P.H)[v] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         if ((v & 15) == 0) P.scale[row * blocks + (v >> 4)] = scale;
       }

@@ -404,12 +404,12 @@ MIMO_API int mimo_moe_route(const float* logits, const float* bias, int64_t toke
  *   weight       [features], bf16, or fp32 when weight_fp32 != 0
  *   h            bf16 [tokens, features] or NULL (not written); may be x or residual
  *   y            bf16 [tokens, features] or NULL
- *   codes        E4M3 bytes [tokens, features] or NULL: y / scale rounded to
- *                nearest even, from the FP32 y; scale_inv fp32 [tokens,
- *                ceil(features / 128)]: max(max |y| / 448, 2^-126) of each 1 x 128
- *                block, so that mimo_fp8_dequant_blockwise with blocks of 1 x 128
- *                gives y back.  codes needs scale_inv, and one of y and codes is
- *                needed.
+ *   codes        E4M3 bytes [tokens, features] or NULL: the FP32 quotient y / scale
+ *                of the FP32 y and scale, rounded to nearest even; scale_inv fp32
+ *                [tokens, ceil(features / 128)]: max(max |y| / 448, 2^-126) of each
+ *                1 x 128 block, so that mimo_fp8_dequant_blockwise with blocks of
+ *                1 x 128 gives y back.  codes needs scale_inv, and one of y and
+ *                codes is needed.
  * Sums are FP32.  features: a multiple of 8 (16 with codes) up to 16384, else
  * MIMO_ERR_UNSUPPORTED; 1e-18 <= eps <= 1e18.  But for h, outputs may not
  * overlap inputs.  A NaN in a row makes its y NaN.  Does not synchronise.

@@ -23,7 +23,7 @@ def pytest_configure(config):
 # suite under -x.
 _GPU_MODULE_ORDER = ("test_gpu_parity.py", "test_gpu_full_tensor.py", "test_gpu_decode.py",
                      "test_gpu_decode_tiles.py", "test_gpu_neighbors.py", "test_gpu_bwd.py", "test_gpu_bwd_tc.py",
-                     "test_gpu_steps.py", "test_zz_no_alloc.py")
+                     "test_gpu_steps.py", "test_gpu_step_edges.py", "test_zz_no_alloc.py")
 
 
 def pytest_collection_modifyitems(session, config, items):

@@ -1,0 +1,41 @@
+"""The layer's steps at values and sizes where they are easily wrong, on the CPU (tests/step_edges.py)."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+EMU = os.path.join(HERE, "host_emulation")
+sys.path.insert(0, EMU)
+import build_library  # noqa: E402
+import step_edges  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def host_library(tmp_path_factory):
+    return build_library.build(str(tmp_path_factory.mktemp("edges_host")),
+                               flags=("-fsanitize=alignment", "-fno-sanitize-recover=alignment"))
+
+
+def run(lib, names, sms=None):
+    env = dict(os.environ, HEMU_SMS=str(sms)) if sms else None
+    r = subprocess.run([sys.executable, os.path.join(EMU, "edge_cases.py"), lib, *names], capture_output=True, text=True,
+                       timeout=900, env=env)
+    return r.returncode, (r.stdout + r.stderr)[-2000:]
+
+
+@pytest.mark.parametrize("name", sorted(step_edges.CASES))
+def test_edges(host_library, name):
+    rc, log = run(host_library, [name])
+    assert rc == 0, log
+
+
+def test_e4m3_codes_against_torch():
+    """The tests' own rounding to E4M3."""
+    import torch
+    rng = np.random.default_rng(3)
+    grid = step_edges.e4m3_to_f64(np.arange(0x7F, dtype=np.uint8))
+    q = np.concatenate([rng.uniform(-448, 448, 4000), rng.uniform(-0.1, 0.1, 1000), grid, -(grid[1:] + grid[:-1]) / 2]).astype(np.float32)
+    assert np.array_equal(step_edges.e4m3_codes(q), torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
