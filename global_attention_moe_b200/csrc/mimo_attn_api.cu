@@ -831,8 +831,12 @@ void launch_route_bwd(const rg::RouteBwdParams& P, int sms, cudaStream_t stream)
   const long long blocks = (P.T + rg::kWarps * per_warp - 1) / (rg::kWarps * per_warp);
   const unsigned grid = (unsigned)std::min<long long>(blocks, 32LL * sms);
   const size_t smem = (size_t)rg::kWarps * ((per_warp * P.E + 3) / 4 * 4) * 4;
-  if (dense)
-    rg::route_bwd_dense_kernel<<<grid, rg::kThreads, 0, stream>>>(P);
+  if (dense && P.E <= 128)
+    rg::route_bwd_dense_kernel<4><<<grid, rg::kThreads, 0, stream>>>(P);
+  else if (dense && P.E <= 256)
+    rg::route_bwd_dense_kernel<8><<<grid, rg::kThreads, 0, stream>>>(P);
+  else if (dense)
+    rg::route_bwd_dense_kernel<16><<<grid, rg::kThreads, 0, stream>>>(P);
   else if (W == 8)
     rg::route_bwd_sparse_kernel<8><<<grid, rg::kThreads, smem, stream>>>(P);
   else if (W == 16)

@@ -768,56 +768,50 @@ struct RouteBwdParams {
   float scale;
 };
 
-// Gradient of the weights with respect to the logits (the choice itself has none).  With g = dw, p_j =
-// s_j / sum of the chosen s and gm = sum_i g_i p_i:
-//   sigmoid, normalised   dx_j = scale (g_j - gm) p_j (1 - s_j)      (from ds_j = scale (g_j - gm) / S)
-//   sigmoid               dx_j = scale g_j s_j (1 - s_j)
-//   softmax, normalised   dx_j = scale (g_j - gm) p_j                (the softmax's own sum cancels)
-//   softmax               dx_e = scale s_e (sum of g_j with id_j = e - sum_j g_j s_j)     every expert
-// An id outside [0, E) is an empty place: it takes no part.  The same id twice adds up, in the order of the
-// places.  p and the derivatives are formed in FP32 from e^-|x| (1 - s is formed as a score, not by
-// subtraction); a token whose chosen scores all fall below e^-60 takes FP64, where FP32 would lose them.
+// Gradient of the weights with respect to the logits (the choice itself has none).  With g = scale dw and p_j =
+// s_j / sum of the chosen s:
+//   sigmoid, normalised   dx_j = p_j (1 - s_j) (g_j - sum_i g_i p_i)
+//   sigmoid               dx_j = g_j s_j (1 - s_j)
+//   softmax, normalised   dx_j = p_j (g_j - sum_i g_i p_i)             (the softmax's own sum cancels)
+//   softmax               dx_e = s_e (g_e - sum_i g_i s_i)             every expert, g_e = 0 for those not chosen
+// Where one expert has nearly all of the sum, g_j and the mean agree in all bits that FP32 has, and what is left
+// is the row.  So the differences are formed first: with D the chosen expert of the largest logit and
+// dev_i = g_i - g_D (zero for D), g_j - sum_i g_i p_i = dev_j - sum_i p_i dev_i, where no term but D's has a p
+// above one half; for the plain softmax, with C and U the scores of the chosen and of the others (C + U = 1),
+// g_j - sum_i g_i s_i = g_j U + C dev_j - sum_i s_i dev_i.  1 - s is formed as a score, not by subtraction.
+// An id outside [0, E) is an empty place: it takes no part.  The same id several times is one place with the sum of
+// the gradients: score m s and the mean gradient for m places.
+//
+// FP32 throughout: sigmoid scores below one half enter p as e^(x - max x), so that p is as exact far below zero;
+// plain sigmoid scores that FP32 does not hold (x below -80) are formed in FP64.
 //
 // Both kernels are bound by the rows they write.
 
-// The place's peers: the lanes with the same id (empty places: alone).  Returns, in every lane, the sum of v
-// over the peers in the order of the lanes, and whether this lane is the first of them.
-__device__ __forceinline__ float sum_same(float v, int tag, int lane, bool& lead) {
+// The places of one expert (lanes with the same tag; empty places: tags of their own) become one: the first takes
+// the mean (kMean) or the sum of their gradients and their number, the others are emptied.  The result is in two
+// floats, g + rest, so that its difference from another's is as exact as that of single places.
+template <bool kMean>
+__device__ __forceinline__ void join_same(int tag, int lane, bool& has, float& g, float& rest, float& count) {
+  count = 1.f;
+  rest = 0.f;
   const unsigned peers = __match_any_sync(0xffffffffu, tag);
-  lead = __ffs(peers) - 1 == lane;
-  if (__all_sync(0xffffffffu, peers == (1u << lane))) return v;
-  float s = 0.f;
+  if (__all_sync(0xffffffffu, peers == (1u << lane))) return;
+  double s = 0.0;
   for (int j = 0; j < 32; ++j) {
-    const float o = __shfl_sync(0xffffffffu, v, j);
-    if ((peers >> j) & 1u) s += o;
+    const float o = __shfl_sync(0xffffffffu, g, j);
+    if ((peers >> j) & 1u) s += static_cast<double>(o);
   }
-  return s;
+  count = static_cast<float>(__popc(peers));
+  if (kMean) s /= static_cast<double>(count);
+  has = has && __ffs(peers) - 1 == lane;
+  g = has ? static_cast<float>(s) : 0.f;
+  if (has && fabsf(g) < INFINITY) rest = static_cast<float>(s - static_cast<double>(g));
 }
 
-// d w_j / d x_j times g, less the means, for W places of a token in W lanes, in FP64 (few tokens).
-template <int W>
-__device__ __noinline__ float bwd_place_f64(int softmax, int normalize, float g, float x, bool has) {
-  auto sum = [](double v) {
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  };
-  const double xd = static_cast<double>(x), gd = static_cast<double>(g);
-  double s = 0.0, c = 1.0;
-  if (softmax) {
-    double mx = has ? xd : -INFINITY;
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    s = has && mx > -INFINITY ? exp(xd - mx) : 0.0;
-  } else if (has) {
-    s = nb::route_sigmoid_f64(xd);
-    c = nb::route_sigmoid_f64(-xd);
-  }
-  if (!normalize) return static_cast<float>(gd * s * c);
-  const double S = sum(s);
-  const double p = S == 0.0 ? 0.0 : s / S;
-  const double gm = sum(has ? gd * p : 0.0);
-  return static_cast<float>((gd - gm) * p * c);
+// s (1 - s) g of a sigmoid score, in FP64 (few places).
+__device__ __noinline__ float sigmoid_place_f64(float g, float x) {
+  const double xd = static_cast<double>(x);
+  return static_cast<float>(static_cast<double>(g) * nb::route_sigmoid_f64(xd) * nb::route_sigmoid_f64(-xd));
 }
 
 // All but the plain softmax: few elements of a row are not zero.  W lanes to a token (top_k <= W), 32 / W
@@ -836,48 +830,47 @@ __global__ void __launch_bounds__(kThreads) route_bwd_sparse_kernel(const __grid
   for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens; t0 < P.T; t0 += step) {
     const int64_t tok = t0 + sub;
     int id = -1;
-    float g = 0.f, x = -INFINITY;
+    float g = 0.f, x = -INFINITY, rest, count;
     if (tok < P.T && j < P.top_k) {
       id = __ldg(P.ids + tok * P.top_k + j);
-      g = __ldg(P.dweights + tok * P.top_k + j) * P.scale;
+      g = __ldg(P.dweights + tok * P.top_k + j);
       if (id < 0 || id >= P.E) id = -1;
       if (id >= 0) x = __ldg(P.logits + tok * P.E + id);
       else g = 0.f;
     }
-    const bool has = id >= 0;
+    bool has = id >= 0;
+    join_same<true>(has ? sub * P.E + id : -1 - lane, lane, has, g, rest, count);
     auto sum = [](float v) {
 #pragma unroll
       for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
     };
-    float mx = x;
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // sigmoid: r is the larger of s and 1 - s, e r the smaller
+    const float e = P.softmax ? 0.f : expf(-fabsf(x)), r = P.softmax ? 1.f : __fdiv_rn(1.f, 1.f + e);
+    const float c = P.softmax ? 1.f : x >= 0.f ? e * r : r;
     float d;
-    if (__any_sync(0xffffffffu, has && !P.softmax && !(mx > -60.f))) {  // NaN too
-      d = bwd_place_f64<W>(P.softmax, P.normalize, g, x, has);
+    if (P.normalize) {
+      float mx = has ? x : -INFINITY;
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const unsigned tops = __ballot_sync(0xffffffffu, has && x == mx) >> (sub * W) & (0xffffffffu >> (32 - W));
+      const int D = sub * W + (tops ? __ffs(tops) - 1 : j);
+      const float diff = (g - __shfl_sync(0xffffffffu, g, D)) + (rest - __shfl_sync(0xffffffffu, rest, D));
+      const float dev = has ? diff * P.scale : 0.f;
+      const float base = P.softmax ? mx : fminf(mx, 0.f);
+      float s = !P.softmax && x >= 0.f ? r : base == 0.f ? e * r : expf(x - base) * r;
+      s = has && mx > -INFINITY ? s * count : 0.f;
+      if (has && x != x) s = x;
+      const float S = sum(s);
+      const float p = S == 0.f ? 0.f : __fdiv_rn(s, S);
+      d = (dev - sum(p * dev)) * p * c;
     } else {
-      float s, c = 1.f;
-      if (P.softmax) {
-        s = has && mx > -INFINITY ? expf(x - mx) : 0.f;
-      } else {
-        const float e = expf(-fabsf(x)), r = __fdiv_rn(1.f, 1.f + e);
-        s = has ? (x >= 0.f ? r : e * r) : 0.f;
-        c = x >= 0.f ? e * r : r;
-        if (x != x) s = x;
-      }
-      if (P.normalize) {
-        const float S = sum(s);
-        const float p = S == 0.f ? 0.f : __fdiv_rn(s, S);
-        d = (g - sum(g * p)) * p * c;
-      } else {
-        d = g * s * c;
-      }
+      g *= count * P.scale;
+      d = g * (x >= 0.f ? r : e * r) * c;
+      if (__any_sync(0xffffffffu, has && x < -80.f && x > -INFINITY) && has && x < -80.f) d = sigmoid_place_f64(g, x);
     }
-    bool lead;
-    d = sum_same(d, has ? sub * P.E + id : -1 - lane, lane, lead);
     float* at = rows + sub * P.E + id;
-    if (has && lead) *at = d;
+    if (has) *at = d;
     __syncwarp();
     const int64_t left = (P.T - t0) * P.E;
     float* out = P.dlogits + t0 * P.E;
@@ -889,58 +882,78 @@ __global__ void __launch_bounds__(kThreads) route_bwd_sparse_kernel(const __grid
       for (int e = lane; e < m; e += 32) out[e] = rows[e];
     }
     __syncwarp();
-    if (has && lead) *at = 0.f;
+    if (has) *at = 0.f;
     __syncwarp();
   }
 }
 
-// Softmax weights that were not renormalised: every element of the row.  One warp per token.
+// Softmax weights that were not renormalised: every element of the row.  One warp per token, kM >= E / 32 experts to
+// a lane (with 16 for every E, 128 experts of 4099 tokens take 5.7 us instead of 4.8; 65536 x 256: 59 us).
+template <int kM>
 __global__ void __launch_bounds__(kThreads) route_bwd_dense_kernel(const __grid_constant__ RouteBwdParams P) {
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); tok < P.T; tok += step) {
     const float* x = P.logits + tok * P.E;
-    float v[kMaxPerLane];
+    float v[kM];
     int id = -1;
-    float g = 0.f, xj = -INFINITY;
+    float g = 0.f, xj = -INFINITY, rest, count;
     if (lane < P.top_k) {
       id = __ldg(P.ids + tok * P.top_k + lane);
-      g = __ldg(P.dweights + tok * P.top_k + lane) * P.scale;
+      g = __ldg(P.dweights + tok * P.top_k + lane);
       if (id < 0 || id >= P.E) id = -1;
     }
     float mx = -INFINITY;
 #pragma unroll
-    for (int m = 0; m < kMaxPerLane; ++m)
+    for (int m = 0; m < kM; ++m)
       if (32 * m < P.E) {
         v[m] = lane + 32 * m < P.E ? __ldg(x + lane + 32 * m) : -INFINITY;
         mx = fmaxf(mx, v[m]);
       }
     if (id >= 0) xj = __ldg(x + id);
     else g = 0.f;
-    mx = warp_max(mx);
-    float S = 0.f;
+    bool has = id >= 0;
+    join_same<false>(has ? id : -1 - lane, lane, has, g, rest, count);
+    uint32_t mine = 0;  // bit m: this lane's expert lane + 32 m is chosen
+#pragma unroll 4
+    for (int c = 0; c < P.top_k; ++c) {
+      const int o = __shfl_sync(0xffffffffu, id, c);
+      if (o >= 0 && (o & 31) == lane) mine |= 1u << (o >> 5);
+    }
+    float xm = has ? xj : -INFINITY;
 #pragma unroll
-    for (int m = 0; m < kMaxPerLane; ++m)
+    for (int o = 16; o > 0; o >>= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, o));
+    }
+    const unsigned tops = __ballot_sync(0xffffffffu, has && xj == xm);
+    const int D = tops ? __ffs(tops) - 1 : lane;
+    const float dev = ((g - __shfl_sync(0xffffffffu, g, D)) + (rest - __shfl_sync(0xffffffffu, rest, D))) * P.scale;
+    g *= P.scale;
+    // sums over the exponentials as they are; 1 / (U + C) comes in at the end
+    float U = 0.f;
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
       if (32 * m < P.E) {
         v[m] = lane + 32 * m < P.E ? expf(v[m] - mx) : 0.f;
-        S += v[m];
+        U += (mine >> m) & 1u ? 0.f : v[m];
       }
+    const float s = has ? expf(xj - mx) : 0.f;
+    float C = s, gm = g * s, dm = has ? dev * s : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    const float inv = __fdiv_rn(1.f, S);
-    const float s = id >= 0 ? expf(xj - mx) * inv : 0.f;
-    float gm = g * s;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) gm += __shfl_xor_sync(0xffffffffu, gm, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      U += __shfl_xor_sync(0xffffffffu, U, o);
+      C += __shfl_xor_sync(0xffffffffu, C, o);
+      gm += __shfl_xor_sync(0xffffffffu, gm, o);
+      dm += __shfl_xor_sync(0xffffffffu, dm, o);
+    }
+    const float inv = __fdiv_rn(1.f, U + C), inv2 = inv * inv;
     float* out = P.dlogits + tok * P.E;
-    const float f = -gm * inv;
+    const float f = -gm * inv2;
 #pragma unroll
-    for (int m = 0; m < kMaxPerLane; ++m)
-      if (lane + 32 * m < P.E) out[lane + 32 * m] = f * v[m];
-    bool lead;
-    const float gs = sum_same(g, id >= 0 ? id : -1 - lane, lane, lead);
-    __syncwarp();  // the row's stores above come before those of the chosen experts
-    if (id >= 0 && lead) out[id] = s * (gs - gm);
+    for (int m = 0; m < kM; ++m)
+      if (lane + 32 * m < P.E && !((mine >> m) & 1u)) out[lane + 32 * m] = f * v[m];
+    if (has) out[id] = s * inv2 * (fmaf(g, U, C * dev) - dm);
   }
 }
 

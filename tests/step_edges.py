@@ -6,7 +6,7 @@ from __future__ import annotations
 import numpy as np
 
 from oracle.neighbors import e4m3_to_f64
-from step_checks import bits
+from step_checks import bits, close
 
 
 # ---------------------------------------------------------------- RMS norm: the FP8 codes
@@ -49,7 +49,134 @@ def fp8_codes(be):
         assert not off.any(), f"{off.sum()} of {off.size} codes of {H} columns, first at {tuple(np.argwhere(off)[0])}"
 
 
+# ---------------------------------------------------------------- the router's gradient where one expert dominates
+def route_bwd_terms(x, ids, g, softmax, normalize, scale):
+    """(dlogits, tolerance) of one token in FP64, from differences of the gradients g, so that nothing is lost where
+    one expert has nearly the whole sum.  With an expert's m places taken together (g: their mean):
+      normalised       d_e = scale c_e p_e sum_i p_i (g_e - g_i),   p = m s / sum m s,  c = 1 - s (sigmoid) or 1
+      plain sigmoid    d_e = scale m g_e s_e c_e
+      plain softmax    d_e = scale s_e (m_e g_e U + sum_i s_i (m_e g_e - m_i g_i)) for a chosen e, U the score of all
+                       that are not, and -scale s_e sum_i s_i m_i g_i for those
+    The tolerance counts roundings of FP32 operations, on the magnitudes of the terms with the differences taken from
+    the chosen expert of the largest logit: an exponential of t = x - max is off by 2^-24 |t| (the subtraction) and
+    2^-23, a sum of n terms by n 2^-24 (n 32 for the places, 512 / 32 + 5 for a row), quotients and products by a
+    few; 64 + |t| in all.  Gradients of one expert's places are added in two floats: 2^-46 of their magnitude.  Below 2^-126 FP32 has its own spacing."""
+    E, xd = len(x), x.astype(np.float64)
+    d, tol = np.zeros(E), np.zeros(E)
+    places = {}
+    for i, v in zip(ids, g.astype(np.float64)):
+        if 0 <= i < E:
+            places.setdefault(int(i), []).append(v)
+    e = np.array(sorted(places), dtype=int)
+    if len(e) == 0:
+        return d, tol
+    m, total = np.array([len(places[i]) for i in e], dtype=float), np.array([sum(places[i]) for i in e])
+    top = int(np.argmax(xd[e]))
+    u = 2.0 ** -24
+    with np.errstate(over="ignore", under="ignore"):
+        near = np.exp(-np.abs(xd))
+        s = np.where(xd >= 0, 1, near) / (1 + near)
+        c = np.where(xd >= 0, near, 1) / (1 + near)
+        if softmax and not normalize:
+            t = np.minimum(np.abs(xd - xd.max()), 1000)  # (-inf: a score of zero)
+            s = np.exp(-t) / np.exp(-t).sum()
+            others = np.ones(E, dtype=bool)
+            others[e] = False
+            U, gm = s[others].sum(), (s[e] * total).sum()
+            d, tol = -s * gm, s * (64 + t) * u * (s[e] * np.abs(total) * (1 + t[e])).sum()
+            d[e] = [s[i] * (G * U + (s[e] * (G - total)).sum()) for i, G in zip(e, total)]
+            dev = np.abs(total - total[top]) + np.where(m.max() > 1, np.abs(total) + np.abs(total[top]), 0) * u * 4 * u / (64 * u)
+            tol[e] = s[e] * (64 + t[e] + U * t.max()) * u * (np.abs(total) * U + s[e].sum() * dev + (s[e] * dev * (1 + t[e])).sum())
+        elif not normalize:
+            d[e] = total * s[e] * c[e]
+            tol[e] = np.abs(d[e]) * 16 * u
+        else:
+            t = np.maximum(xd[e] - xd[e].max(), -1000)
+            if softmax:
+                p = m * np.exp(t)
+            else:  # s = exp(min(x, 0)) / (1 + exp(-|x|)); a common factor cancels
+                p = m * np.exp(np.minimum(xd[e], 0) - min(xd[e].max(), 0)) / (1 + near[e])
+            p = p / p.sum()
+            G, t, k = total / m, np.abs(t), 1.0 if softmax else c[e]
+            d[e] = k * p * np.array([(p * (v - G)).sum() for v in G])
+            dev = np.abs(G - G[top]) + np.where(m.max() > 1, np.abs(G) + np.abs(G[top]), 0) * u * 4 * u / (64 * u)
+            tol[e] = k * p * (64 + t) * u * (dev + (p * dev * (1 + t)).sum())
+    return scale * d, np.abs(scale) * tol + 2.0 ** -140
+
+
+def check_gradient(be, x, ids, g, softmax, normalize, scale=2.5):
+    d = be.route_bwd(x, ids, g, softmax, normalize, scale)
+    for t in range(len(x)):
+        ref, tol = route_bwd_terms(x[t], ids[t], g[t], softmax, normalize, scale)
+        close(d[t], ref, tol, f"dlogits of token {t} (softmax {softmax}, normalised {normalize}, logits of the chosen {x[t][ids[t] % len(x[t])]})")
+
+
+FORMS = ((False, True), (False, False), (True, True), (True, False))
+
+
+def peaked(T, E, k, gap, seed, level=0.0):
+    """Logits about `level`, one chosen expert `gap` above the other chosen; gradients of like size."""
+    rng = np.random.default_rng(seed)
+    x = (level + rng.standard_normal((T, E))).astype(np.float32)
+    ids = np.argsort(rng.random((T, E)), -1)[:, :k].astype(np.int32)
+    at = np.arange(T), ids[np.arange(T), rng.integers(0, k, T)]
+    x[at] = (x.max(-1) + gap).astype(np.float32)
+    return x, ids, rng.standard_normal((T, k)).astype(np.float32)
+
+
+def gradient_peaked(be):
+    """One expert has nearly all of the chosen experts' sum (or of the softmax): the row is what the others leave."""
+    for gap in (0, 4, 8, 14, 20, 45, 80):
+        for E, k in ((128, 6), (60, 12), (512, 32)):
+            for softmax, normalize in FORMS:
+                for level in (0.0, -gap) if not softmax else (0.0,):
+                    check_gradient(be, *peaked(5, E, k, gap, 200 + gap + E, level), softmax, normalize)
+
+
+def gradient_levels(be):
+    """Sigmoid scores far below one: chosen logits on both sides of -60 and -80, and one far above the others."""
+    for level, gap in ((-30, 20), (-58, 10), (-62, 10), (-70, 5), (-70, 60), (-85, 10), (-100, 30), (-100, 100)):
+        for E, k in ((64, 4), (96, 16)):
+            for normalize in (True, False):
+                check_gradient(be, *peaked(4, E, k, gap, 300 - level + gap, level), False, normalize)
+
+
+def gradient_alike(be):
+    """Chosen experts whose gradients are alike: normalised rows are zero, plain softmax rows what the others hold."""
+    for softmax, normalize in FORMS:
+        x, ids, g = peaked(4, 64, 8, 0, 400)
+        g[:] = g[:, :1]
+        x[np.arange(4)[:, None], ids[:, :2]] = 20.0  # two that share nearly the whole
+        check_gradient(be, x, ids, g, softmax, normalize)
+        if normalize:
+            assert np.all(be.route_bwd(x, ids, g, softmax, normalize, 2.5) == 0)
+    x, ids, g = peaked(3, 64, 1, 5, 401)
+    for softmax in (False, True):
+        assert np.all(be.route_bwd(x, ids, g, softmax, True, 1.0) == 0)  # one place: its weight is the scale
+
+
+def gradient_places(be):
+    """The same expert in two and more places, empty places, the dominating expert among them; switched-off experts."""
+    x, _, g = peaked(6, 64, 6, 0, 500)
+    ids = np.array([[3, 3, 9, 10, -1, 64], [3, 9, 3, 11, 9, 2], [5, 5, 5, 5, 6, 7], [-1, -1, -1, -1, -1, 8],
+                    [-1, -7, 64, 99, -1, -1], [0, 1, 2, 3, 4, 63]], dtype=np.int32)
+    for gap in (0, 14, 30):
+        for at in (3, 9, 5, 63):
+            z = x.copy()
+            z[:, at] += np.float32(gap)
+            for softmax, normalize in FORMS:
+                check_gradient(be, z, ids, g, softmax, normalize)
+    x[:, ::2] = -np.inf
+    x[:, 1::4] = np.finfo(np.float32).min
+    for softmax, normalize in FORMS:
+        check_gradient(be, x, np.array([[1, 2, 3, 7, 11, 0]] * 6, dtype=np.int32), g, softmax, normalize)
+
+
 # Cases by name.
 CASES = {
+    "gradient_peaked": gradient_peaked,
+    "gradient_levels": gradient_levels,
+    "gradient_alike": gradient_alike,
+    "gradient_places": gradient_places,
     "fp8_codes": fp8_codes,
 }

@@ -39,3 +39,23 @@ def test_e4m3_codes_against_torch():
     grid = step_edges.e4m3_to_f64(np.arange(0x7F, dtype=np.uint8))
     q = np.concatenate([rng.uniform(-448, 448, 4000), rng.uniform(-0.1, 0.1, 1000), grid, -(grid[1:] + grid[:-1]) / 2]).astype(np.float32)
     assert np.array_equal(step_edges.e4m3_codes(q), torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+@pytest.mark.parametrize("softmax,normalize", step_edges.FORMS)
+def test_gradient_terms_against_the_definition(softmax, normalize):
+    """The gradient from differences is the chain rule's (oracle/steps.py), where that loses nothing in FP64, and
+    that of torch's autograd."""
+    import torch
+    from oracle import steps
+    for gap in (0, 4, 8):
+        x, ids, g = step_edges.peaked(6, 40, 5, gap, gap)
+        if gap == 4:
+            ids[0, :2], ids[1, 3] = ids[0, 0], -1
+        ref = steps.route_bwd(x, ids, g, softmax, normalize, 2.5)
+        got = np.stack([step_edges.route_bwd_terms(x[t], ids[t], g[t], softmax, normalize, 2.5)[0] for t in range(6)])
+        assert np.abs(got - ref).max() < 1e-10
+        if gap != 4:
+            t = torch.tensor(x, dtype=torch.float64, requires_grad=True)
+            s = (torch.softmax(t, -1) if softmax else torch.sigmoid(t)).gather(1, torch.tensor(ids.astype(np.int64)))
+            (2.5 * (s / s.sum(-1, keepdim=True) if normalize else s) * torch.tensor(g, dtype=torch.float64)).sum().backward()
+            assert np.abs(got - t.grad.numpy()).max() < 1e-10
