@@ -25,6 +25,7 @@ namespace ev {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;  // CTAs to a sequence
 constexpr int kBins = 2048;
 constexpr int kAhead = 8;  // loads of 32 entries that a warp has in flight
 constexpr uint32_t kMust = 0xFFFFFFFFu;  // above every weight's bits

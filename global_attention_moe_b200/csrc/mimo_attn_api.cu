@@ -758,9 +758,10 @@ void launch_norm_bwd(const rms::NormBwdParams& P, bool w32, unsigned grid, cudaS
     rms::rms_norm_bwd_kernel<TPR, V, uint16_t><<<grid, rms::kBwdThreads, smem, stream>>>(P);
 }
 
-// An index list's entries for the key weights and the eviction, whose kernels count in int and step up to 256
-// entries past an end.
-constexpr int kMaxListEntries = 0x7FFFF000;
+// An index list's entries for the key weights and the eviction, whose kernels count in int: the widest step past an
+// end is that of the eviction's copy, all threads of a cluster.
+constexpr int kMaxListEntries = 0x7FFFC000;
+static_assert(kMaxListEntries <= INT32_MAX - ev::kMaxCluster * ev::kThreads, "the eviction's loops");
 
 // ---------------------------------------------------------------- routing
 // The kernel of four threads per token: whole blocks of eight experts to a group, at most eight groups and
@@ -872,7 +873,7 @@ int launch_evict(ev::EvictParams& P, cudaStream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MIMO_ERR_CUDA;
   if (P.max_kv_len <= 2048) return launch_evict_c<1>(P, dev, stream);
   if (P.max_kv_len <= 16384) return launch_evict_c<2>(P, dev, stream);
-  return launch_evict_c<8>(P, dev, stream);
+  return launch_evict_c<ev::kMaxCluster>(P, dev, stream);
 }
 
 // ---------------------------------------------------------------- key weights

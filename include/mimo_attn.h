@@ -489,7 +489,7 @@ MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const f
  * mimo_decode_key_weights_workspace_size(dims) bytes (0 for invalid dims; about
  * 516 bytes per new token and query head, and 4 per key and KV head, up to 32 times
  * that where a sequence's queries fill several tiles and there are few keys); calls
- * that overlap need one each.  total_kv at most 2^31 - 4096 (else
+ * that overlap need one each.  total_kv at most 2^31 - 16384 (else
  * MIMO_ERR_UNSUPPORTED).  Does not synchronise.
  */
 MIMO_API size_t mimo_decode_key_weights_workspace_size(const mimo_decode_dims* dims);
@@ -513,7 +513,7 @@ MIMO_API int mimo_decode_key_weights(const void* q, const void* k_cache, const i
  *               start at kv_indptr[b] - new_indptr[b]
  * Outputs are written up to the new totals only, and may not overlap inputs.
  * 0 <= keep_first, 0 <= keep_recent, keep_first + keep_recent <= budget; at most
- * 65536 sequences and 2^31 - 4096 entries (else MIMO_ERR_UNSUPPORTED).  An
+ * 65536 sequences and 2^31 - 16384 entries (else MIMO_ERR_UNSUPPORTED).  An
  * inconsistent kv_indptr is recorded as MIMO_ERR_BAD_SEQLENS and nothing is
  * written.  The positions of the keys that stay move up with them (a key's
  * position is its place in the list).  Does not synchronise.
