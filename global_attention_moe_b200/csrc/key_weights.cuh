@@ -22,7 +22,7 @@
 //      N columns, so that a thread owns one key (a TMEM lane) and adds that key's exponentials in a
 //      register, with no reduction across threads.  Each unit writes its sums to a partial row [f, KV
 //      head][key];
-//   3. kw_join_kernel: adds the partial rows in a fixed order, and prev.
+//   3. kw_join_kernel: adds the partial rows in a fixed order, and prev; writes nothing if launch 2 gave up.
 //
 // Warp roles of the main kernel (24 warps; registers are dealt out by warpgroup):
 //   warp 0       TMEM owner; issues the MMAs (A = K from TMEM, B = Q from shared memory)
@@ -78,7 +78,7 @@ struct Params {
   float* out;                 // [total_kv]
   uint16_t* qs;               // workspace: [hkv * Tq * group, 256]
   float* lse2;                // workspace: [hkv * Tq * group], log2 units
-  long long* units;           // workspace: [num_seqs + 1], running count of units
+  long long* units;           // workspace: [num_seqs + 1], running count of units; then whether launch 2 gave up
   float* partial;             // workspace: [parts * hkv, total_kv]
   int32_t num_seqs, total_q, total_kv, cache_rows, max_q_len, max_kv_len;
   int32_t hq, hkv, group;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kPrepThreads) kw_prep_kernel(const __grid_cons
       for (int k = 0; k < kPrepThreads / 32; ++k) before += s_warp[k];
       __syncthreads();
     }
-    if (threadIdx.x == 0) P.units[0] = 0;
+    if (threadIdx.x == 0) P.units[0] = P.units[P.num_seqs + 1] = 0;
     if (bad) atomicOr(&g_mimo_error, kErrSeqlens);
     return;
   }
@@ -725,7 +725,10 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
     skip = (*reinterpret_cast<volatile unsigned int*>(&g_mimo_error) & kErrTimeout) != 0;
     if (smem_u32(smem) & 1023u) skip = 1;  // swizzled operands need a 1 KB aligned base
   }
-  if (__syncthreads_or(skip)) return;
+  if (__syncthreads_or(skip)) {
+    if (tid == 0) P.units[P.num_seqs + 1] = 1;
+    return;
+  }
   if (tid == 0) {
     for (int s = 0; s < KS; ++s) {
       mbar_init(&C->k_landed[s], 128);  // one cp.async arrival per fetcher thread
@@ -787,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) kw_main_kernel(const __grid_const
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
+  if (tid == 0 && *reinterpret_cast<volatile int*>(&C->abort)) P.units[P.num_seqs + 1] = 1;
   if (warp == 0) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
@@ -810,7 +814,9 @@ __global__ void __launch_bounds__(kJoinThreads) kw_join_kernel(const __grid_cons
   const float p = in && P.prev != nullptr ? P.prev[i] : 0.f;
   // the sequence of the warp's first entry, and from there on to this entry's
   const long long i0 = i - lane;
-  if (i0 >= P.total_kv) return;
+  // where launch 2 gave up (a bounded wait ran out, in it or before it) partial rows are missing: out, which may be
+  // prev, stays as it was
+  if (i0 >= P.total_kv || P.units[P.num_seqs + 1] != 0) return;
   int b = find_seq(P.kv_indptr, P.num_seqs, static_cast<int>(i0), lane);
   if (!in) return;
   while (b + 1 < P.num_seqs && __ldg(P.kv_indptr + b + 1) <= i) ++b;

@@ -901,7 +901,7 @@ KeyWeightsPlan key_weights_plan(const mimo_decode_dims* d) {
   p.qs = 0;
   p.lse2 = p.qs + align256(qrows * 512);
   p.units = p.lse2 + align256(qrows * 4);
-  p.partial = p.units + align256(((size_t)d->num_seqs + 1) * 8);
+  p.partial = p.units + align256(((size_t)d->num_seqs + 2) * 8);
   p.bytes = p.partial + align256((size_t)p.parts * d->num_kv_heads * d->total_kv * 4);
   return p;
 }

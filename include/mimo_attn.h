@@ -484,7 +484,9 @@ MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const f
  * Range of rotated values as the forward's (MIMO_ERR_RANGE).  Inconsistent
  * sequences are recorded as MIMO_ERR_BAD_SEQLENS and left unwritten, as are
  * entries behind the last sequence; cache rows outside [0, cache_rows) count as
- * zeros and are recorded.
+ * zeros and are recorded.  Where a bounded wait ran out, in this call or in one
+ * before it (MIMO_ERR_TIMEOUT, until mimo_attn_check has returned it), out is left
+ * as it was.
  * workspace: device, 256-byte aligned, at least
  * mimo_decode_key_weights_workspace_size(dims) bytes (0 for invalid dims; about
  * 516 bytes per new token and query head, and 4 per key and KV head, up to 32 times

@@ -19,6 +19,7 @@ extern "C" {
 __attribute__((visibility("default"))) void* hemu_alloc(size_t n) { return hemu::guarded_alloc(n); }
 __attribute__((visibility("default"))) void hemu_free(void* p) { hemu::guarded_free(p); }
 __attribute__((visibility("default"))) int hemu_errors(void) { return hemu::g_errors; }
+__attribute__((visibility("default"))) void hemu_set_timeout(void) { mimo::g_mimo_error |= mimo::kErrTimeout; }
 }
 '''
 

@@ -59,3 +59,43 @@ def test_gradient_terms_against_the_definition(softmax, normalize):
             s = (torch.softmax(t, -1) if softmax else torch.sigmoid(t)).gather(1, torch.tensor(ids.astype(np.int64)))
             (2.5 * (s / s.sum(-1, keepdim=True) if normalize else s) * torch.tensor(g, dtype=torch.float64)).sum().backward()
             assert np.abs(got - t.grad.numpy()).max() < 1e-10
+
+
+GAVE_UP = """
+import sys
+import numpy as np
+from step_cases import Host
+import step_checks as S
+be = Host(sys.argv[1])
+for q_lens in ([1, 3], [90, 40]):  # one query tile to a sequence, and several
+    q, k, idx, indptr, cu_q = S.step_batch([300, 150], q_lens, 8, 2, 1)
+    lse = np.ones((8, sum(q_lens)), dtype=np.float32)
+    prev = np.arange(450, dtype=np.float32)
+    if sys.argv[2] == "before":
+        be.L.hemu_set_timeout()
+    out = be.key_weights(q, k, idx, indptr, cu_q, lse, max(q_lens), 300, -1, 1e7, prev, errors=True, fill=-7.0)
+    assert be.status == 4, be.status  # MIMO_ERR_TIMEOUT
+    assert np.all(out == -7), out
+    if sys.argv[2] == "before":  # the next call works again
+        a = be.key_weights(q, k, idx, indptr, cu_q, lse, max(q_lens), 300, -1, 1e7, prev)
+        S.close(a, S.steps.key_weights(q, k, idx, indptr, cu_q, lse, -1, 1e7, prev),
+                S.weights_tolerance(q, k, idx, indptr, cu_q, lse, -1, 1e7, prev), "after")
+"""
+
+
+def gave_up(lib, *args):
+    r = subprocess.run([sys.executable, "-c", GAVE_UP, lib, *args], capture_output=True, text=True, timeout=600, cwd=EMU)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-2000:]
+
+
+def test_key_weights_after_a_timeout_leave_out_alone(host_library):
+    """The status of a wait that ran out earlier is set: the product kernel does not run, and the sums that it did
+    not write do not reach out."""
+    gave_up(host_library, "before")
+
+
+def test_key_weights_whose_wait_runs_out_leave_out_alone(tmp_path):
+    """A wait inside the call runs out (planted: all have a limit of zero)."""
+    lib = build_library.build(str(tmp_path), mutations=[(
+        "mimo_attn_api.cu", "constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;", "constexpr uint64_t kDefaultWaitLimitNs = 0ull;")])
+    gave_up(lib, "inside")
