@@ -9,9 +9,11 @@
 // the sink's share).
 //
 // Precision: the weights are FP32 and are summed over many steps, so the scores are formed more exactly
-// than the attention's: the rotated dims of Q and K are each split into an FP16 value and the FP16
-// rounding of what is left (22 bits), and three products hi hi + hi lo + lo hi take the place of one; the
-// pass-through dims are exact in BF16.  Rotation angles come from FP64-reduced positions.
+// than the attention's: the rotated dims of Q and K are each split into an FP16 value and what is left, times
+// 2^11 and rounded to FP16 (22 bits from 2^-14 on, 2^-36 below: unscaled, the rest would run out of FP16's
+// exponents from about 1 down, and queries of 3000 with keys of 3e-4 were off by 1.5e-5).  Three products hi hi +
+// 2^-11 (hi lo + lo hi) take the place of one, the last two first: the MMA that starts hi hi takes the accumulator
+// times 2^-11.  The pass-through dims are exact in BF16.  Rotation angles come from FP64-reduced positions.
 //
 // Three launches:
 //   1. kw_prep_kernel: Q rotated and split once, into rows of 256 16-bit values (hi 64, lo 64, pass 128)
@@ -126,10 +128,12 @@ __device__ __forceinline__ float2 angle(int pos, double theta) {
   return make_float2(c, s);
 }
 
-// x as an FP16 value and the FP16 rounding of the rest.
+constexpr int kLoBits = 11;  // the rest is held times 2^kLoBits, at most as large as x
+
+// x as an FP16 value and the FP16 rounding of the rest, scaled.
 __device__ __forceinline__ void split16(float x, __half& hi, __half& lo) {
   hi = __float2half_rn(x);
-  lo = __float2half_rn(x - __half2float(hi));
+  lo = __float2half_rn((x - __half2float(hi)) * static_cast<float>(1 << kLoBits));
 }
 
 // ---------------------------------------------------------------- launch 1
@@ -491,7 +495,8 @@ __device__ __forceinline__ void role_rotate(uint8_t* smem, Ctrl* C, uint32_t tme
         const __half2 uh = __floats2half2_rn(u.x, u.y), vh = __floats2half2_rn(v.x, v.y);
         amax = __hmax2(amax, __hmax2(__habs2(uh), __habs2(vh)));
         const float2 m1 = make_float2(-1.f, -1.f);
-        const float2 ul = ffma2(__half22float2(uh), m1, u), vl = ffma2(__half22float2(vh), m1, v);
+        const float2 up = make_float2(1 << kLoBits, 1 << kLoBits);
+        const float2 ul = fmul2(ffma2(__half22float2(uh), m1, u), up), vl = fmul2(ffma2(__half22float2(vh), m1, v), up);
         const __half2 uln = __floats2half2_rn(ul.x, ul.y), vln = __floats2half2_rn(vl.x, vl.y);
         ah[4 * q + e] = *reinterpret_cast<const uint32_t*>(&uh);
         al[4 * q + e] = *reinterpret_cast<const uint32_t*>(&uln);
@@ -551,19 +556,19 @@ __device__ __forceinline__ void role_load_q(uint8_t* smem, Ctrl* C, const Params
     wait(C, &C->q_full[i % QS], (i / QS) & 1, P.wait_limit_ns);
 }
 
-// S = K Q^T of one tile: Q hi with K hi and K lo, Q lo with K hi, pass with pass.  k: K's TMEM columns (hi 0, lo
-// 32, pass 64 and 96); q: Q's descriptor (hi, lo, pass, pass, qu apart).  All 20 in a row: the issue of an MMA
-// from a rolled loop takes about 250 cycles, in a row about 90.
+// S = K Q^T of one tile: Q hi with K lo and Q lo with K hi, then, with those times 2^-11, Q hi with K hi, pass with
+// pass.  k: K's TMEM columns (hi 0, lo 32, pass 64 and 96); q: Q's descriptor (hi, lo, pass, pass, qu apart).  All
+// 20 in a row: the issue of an MMA from a rolled loop takes about 250 cycles, in a row about 90.
 __device__ __forceinline__ void issue_tile(uint32_t acc, uint32_t k, uint32_t q, uint32_t qu, uint32_t idesc_f16,
                                            uint32_t idesc_bf16) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + 2 * s, idesc_f16, s > 0 ? 1u : 0u);
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 32 + 8 * s, q + 2 * s, idesc_f16, s > 0 ? 1u : 0u);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 32 + 8 * s, q + 2 * s, idesc_f16, 1u);
-  q += qu;
+  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + qu + 2 * s, idesc_f16, 1u);
+  mma_ts_lo_scaled<kLoBits>(acc, k, q, idesc_f16);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + 2 * s, idesc_f16, 1u);
-  q += qu;
+  for (int s = 1; s < 4; ++s) mma_ts_lo(acc, k + 8 * s, q + 2 * s, idesc_f16, 1u);
+  q += 2 * qu;
 #pragma unroll
   for (int s = 0; s < 4; ++s) mma_ts_lo(acc, k + 64 + 8 * s, q + 2 * s, idesc_bf16, 1u);
   q += qu;

@@ -479,8 +479,9 @@ MIMO_API int mimo_moe_route_bwd(const float* logits, const int32_t* ids, const f
  * key; lse is that call's.  Arguments as mimo_attn_decode (no V, sink in lse);
  * prev fp32 [total_kv] or NULL, out fp32 [total_kv], which may be prev.  Entries
  * whose key no query sees get prev; sequences without new queries are allowed.
- * The scores are formed with the rotated dims to 22 bits (two FP16 parts), and
- * the sums are FP32 in a fixed order: the result does not change from run to run.
+ * The scores are formed with the rotated dims to 22 bits (two FP16 parts; below
+ * 2^-14 to 2^-36), and the sums are FP32 in a fixed order: the result does not
+ * change from run to run.
  * Range of rotated values as the forward's (MIMO_ERR_RANGE).  Inconsistent
  * sequences are recorded as MIMO_ERR_BAD_SEQLENS and left unwritten, as are
  * entries behind the last sequence; cache rows outside [0, cache_rows) count as

@@ -264,6 +264,7 @@ struct MmaOp {
   uint32_t d, a_tmem;
   uint64_t a, b;
   uint32_t idesc, acc;
+  uint32_t down = 0;  // D is taken times 2^-down
 };
 inline std::vector<MmaOp> g_mma_queue;
 
@@ -354,7 +355,10 @@ inline void mma_execute(const MmaOp& op) {
       double s = 0.0;
       for (uint32_t k = 0; k < 16; ++k) s += static_cast<double>(A[m][k]) * B[n][k];
       float acc = 0.f;
-      if (op.acc) std::memcpy(&acc, &T[dl + m % 128][dc + n], 4);
+      if (op.acc) {
+        std::memcpy(&acc, &T[dl + m % 128][dc + n], 4);
+        acc = std::ldexp(acc, -static_cast<int>(op.down));
+      }
       acc = static_cast<float>(acc + s);
       std::memcpy(&T[dl + m % 128][dc + n], &acc, 4);
     }
@@ -443,6 +447,12 @@ inline void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t id
 }
 inline void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   mma_ts(d_tmem, a_tmem, (static_cast<uint64_t>(kDescHiSw128Sbo1K) << 32) | b_lo, idesc, accumulate);
+}
+
+template <int kDown>
+inline void mma_ts_lo_scaled(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+  g_mma_queue.push_back({true, false, hemu::g_cur_cta, d_tmem, a_tmem, 0,
+                         (static_cast<uint64_t>(kDescHiSw128Sbo1K) << 32) | b_lo, idesc, 1u, kDown});
 }
 
 inline uint32_t tmem_addr(uint32_t base, uint32_t lane, uint32_t col) { return base + (lane << 16) + col; }

@@ -5,8 +5,9 @@ from __future__ import annotations
 
 import numpy as np
 
-from oracle.neighbors import e4m3_to_f64
-from step_checks import bits, close
+from oracle import steps
+from oracle.neighbors import bf16_bits_to_f64, e4m3_to_f64
+from step_checks import bits, close, step_batch, weights_tolerance
 
 
 # ---------------------------------------------------------------- RMS norm: the FP8 codes
@@ -172,8 +173,31 @@ def gradient_places(be):
         check_gradient(be, x, np.array([[1, 2, 3, 7, 11, 0]] * 6, dtype=np.int32), g, softmax, normalize)
 
 
+# ---------------------------------------------------------------- key weights of large queries and small keys
+def check_sizes(be, kv_lens, q_lens, hq, hkv, window, base, seed, q_size, k_size):
+    """Queries and keys of any sizes: step_checks.weights_tolerance, and, below the 22 bits that it counts, the
+    rotated values' absolute error of 2^-36 (FP16 down to 2^-14, its rest times 2^11 down to 2^-25)."""
+    q, k, idx, indptr, cu_q = step_batch(kv_lens, q_lens, hq, hkv, seed)
+    scaled = lambda a, f: bits(bf16_bits_to_f64(a) * f)
+    q, k = scaled(q, q_size), scaled(k, k_size)
+    lse = steps.normaliser(q, k, idx, indptr, cu_q, window, base).astype(np.float32)
+    got = be.key_weights(q, k, idx, indptr, cu_q, lse, max(q_lens), max(kv_lens), window, base, None)
+    ref = steps.key_weights(q, k, idx, indptr, cu_q, lse, window, base)
+    tol = weights_tolerance(q, k, idx, indptr, cu_q, lse, window, base, None)
+    # 64 dims of at most sqrt(2) 6 sizes each; a weight is at most one per query and head
+    floor = 64 * 2.0 ** -36 * 9 * (q_size + k_size) / np.sqrt(192.0)
+    close(got, ref, tol + ref * floor, f"key weights, queries of {q_size}, keys of {k_size}")
+
+
+def weights_sizes(be):
+    for q_size, k_size in ((3000.0, 3e-4), (3e-4, 3000.0), (2000.0, 1e-3), (100.0, 0.01), (8000.0, 1e-6), (1e-6, 8000.0), (0.01, 0.01)):
+        check_sizes(be, [130, 40], [1, 3], 8, 2, -1, 1e7, 600, q_size, k_size)
+        check_sizes(be, [200], [70], 4, 2, 128, 1e4, 601, q_size, k_size)
+
+
 # Cases by name.
 CASES = {
+    "weights_sizes": weights_sizes,
     "gradient_peaked": gradient_peaked,
     "gradient_levels": gradient_levels,
     "gradient_alike": gradient_alike,
