@@ -9,8 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-
-import torch
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmimo_attn.so")
@@ -18,6 +17,32 @@ LIB_PATH = os.path.join(HERE, "_build", "libmimo_attn.so")
 LAYER_SWA = 0
 LAYER_GLOBAL = 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_RANGE, ERR_BAD_SEQLENS, ERR_SCRATCH_LIMIT = range(8)
+
+_BF16 = _F32 = _I32 = _raw_stream = None
+
+
+def _use_torch():
+    """Binds torch and what the entry points take from it to this module's names."""
+    global torch, _BF16, _F32, _I32, _raw_stream
+    import torch
+    _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+    # the current stream of a device as an integer: torch.cuda.current_stream() builds a Python stream object
+    # (3.2 us of a 16 us call), this reads the handle (0.1 us); without it the object is built
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+class _Torch:
+    """Stands for torch until its first use: the raw-pointer entry points, the selections and the status calls
+    work without it."""
+
+    def __getattr__(self, name):
+        _use_torch()
+        return getattr(torch, name)
+
+
+torch = _Torch()
+if "torch" in sys.modules:
+    _use_torch()
 
 # Every symbol include/mimo_attn.h declares.
 SYMBOLS = ("mimo_attn_fwd", "mimo_attn_host_workspace_size", "mimo_attn_fwd_host", "mimo_attn_check",
@@ -258,11 +283,6 @@ def make_dims(num_seqs, total_tokens, max_seqlen, hq, hkv, dqk=192, dv=128) -> D
     return Dims(int(num_seqs), int(total_tokens), int(max_seqlen), int(hq), int(hkv), int(dqk), int(dv))
 
 
-# the current stream of a device as an integer: torch.cuda.current_stream() builds a Python stream object
-# (3.2 us of a 16 us call), this reads the handle (0.1 us); without it the object is built
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream_handle(stream):
     if stream is None and _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
@@ -381,9 +401,6 @@ def decode(q, k_cache, v_cache, kv_indices, kv_indptr, cu_q, sink, max_q_len, ma
     if st != OK:
         raise MimoAttnError(st, "mimo_attn_decode")
     return out, lse
-
-
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _refuse(name, t, dtype, shape, dev):
