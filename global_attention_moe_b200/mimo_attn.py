@@ -416,6 +416,12 @@ def _check(name, t, dtype, shape, dev):
         _refuse(name, t, dtype, shape, dev)
 
 
+def _int32(*numbers):
+    """Of a larger number ctypes would pass the low 32 bits."""
+    if max(numbers) > 0x7FFFFFFF or min(numbers) < -0x80000000:
+        raise ValueError(f"a size or choice beyond 32 bits among {numbers}")
+
+
 def _norm_checks(x, name, weight):
     if x.dim() != 2:
         raise ValueError(f"{name} must be [tokens, features], got {tuple(x.shape)}")
@@ -506,6 +512,7 @@ def moe_route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, sc
     ids int32 [T, top_k], weights fp32 [T, top_k] (scale times the scores, normalised to sum to one first)."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
+    _int32(logits.shape[1], top_k, num_groups, top_groups, score)
     dev = torch.cuda.current_device()
     _check("logits", logits, _F32, logits.shape, dev)
     if bias is not None:
@@ -530,6 +537,7 @@ def moe_route_bwd(logits, ids, dweights, score=ROUTE_SIGMOID, normalize=True, sc
     [0, E) is an empty place."""
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError(f"logits and ids must be [tokens, ...], got {tuple(logits.shape)} and {tuple(ids.shape)}")
+    _int32(logits.shape[1], ids.shape[1], score)
     dev = torch.cuda.current_device()
     T, E = logits.shape
     k = ids.shape[1]
@@ -555,10 +563,11 @@ def decode_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, max_q_len, 
     if q.dim() != 3 or k_cache.dim() != 3 or kv_indices.dim() != 1 or cu_q.dim() != 1:
         raise ValueError(f"q and k_cache must be [rows, heads, 192] and the index lists flat, got {tuple(q.shape)}, "
                          f"{tuple(k_cache.shape)}, {tuple(kv_indices.shape)}, {tuple(cu_q.shape)}")
-    dev = torch.cuda.current_device()
     Tq, hq, dqk = q.shape
     rows, hkv, _ = k_cache.shape
     total, B1 = kv_indices.shape[0], cu_q.shape[0]
+    _int32(Tq, rows, total, B1, max_q_len, max_kv_len, layer_kind, window, rope_dims)
+    dev = torch.cuda.current_device()
     _check("q", q, _BF16, q.shape, dev)
     _check("k_cache", k_cache, _BF16, (rows, hkv, dqk), dev)
     _check("kv_indices", kv_indices, _I32, (total,), dev)
@@ -594,8 +603,9 @@ def kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first=0, k
     of which the first new_indptr[B] (freed: the first kv_indptr[B] - new_indptr[B]) are written."""
     if kv_indices.dim() != 1 or kv_indptr.dim() != 1:
         raise ValueError(f"the index lists must be flat, got {tuple(kv_indices.shape)} and {tuple(kv_indptr.shape)}")
-    dev = torch.cuda.current_device()
     total, B1 = kv_indices.shape[0], kv_indptr.shape[0]
+    _int32(total, B1, max_kv_len)
+    dev = torch.cuda.current_device()
     _check("weights", weights, _F32, (total,), dev)
     _check("kv_indices", kv_indices, _I32, (total,), dev)
     _check("kv_indptr", kv_indptr, _I32, (B1,), dev)

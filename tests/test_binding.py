@@ -3,6 +3,8 @@ import os
 import subprocess
 import sys
 
+import pytest
+
 from global_attention_moe_b200 import build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -60,3 +62,37 @@ def test_torch_is_bound_at_its_first_use():
                 "M.torch.float32\n"
                 "assert M.torch is torch and M._BF16 is torch.bfloat16 and M._I32 is torch.int32\n")
         assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr[-2000:]
+
+
+BIG = 2 ** 32
+
+
+@pytest.mark.parametrize("call", [
+    dict(top_k=BIG + 8), dict(num_groups=BIG + 1), dict(top_groups=BIG + 1), dict(score=BIG), dict(score=BIG + 1),
+    dict(num_groups=-BIG + 8), dict(top_k=2 ** 31)])
+def test_router_counts_do_not_wrap(call):
+    import torch
+    build.build()
+    from global_attention_moe_b200 import mimo_attn as M
+    with pytest.raises(ValueError, match="32 bits"):
+        M.moe_route_grouped(torch.zeros(2, 64), None, **call)
+    if "score" in call:
+        with pytest.raises(ValueError, match="32 bits"):
+            M.moe_route_bwd(torch.zeros(2, 64), torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, 8), **call)
+
+
+@pytest.mark.parametrize("call", [
+    dict(max_q_len=BIG + 1), dict(max_kv_len=BIG + 4), dict(layer_kind=BIG), dict(window=BIG + 128), dict(window=-BIG + 128),
+    dict(rope_dims=BIG + 64)])
+def test_key_weight_counts_do_not_wrap(call):
+    import torch
+    build.build()
+    from global_attention_moe_b200 import mimo_attn as M
+    i = torch.zeros(4, dtype=torch.int32)
+    a = dict(max_q_len=1, max_kv_len=4, layer_kind=0, window=128, rope_base=1e4)
+    with pytest.raises(ValueError, match="32 bits"):
+        M.decode_key_weights(torch.zeros(1, 8, 192).bfloat16(), torch.zeros(4, 2, 192).bfloat16(), i, i[:2], i[:2], torch.zeros(8, 1),
+                             **{**a, **call})
+    if "max_kv_len" in call:
+        with pytest.raises(ValueError, match="32 bits"):
+            M.kv_evict(torch.zeros(4), i, i[:2], call["max_kv_len"], 2)
