@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kBulkThreads) route_bulk_kernel(const __grid_c
       all &= __shfl_xor_sync(0xffffffffu, all, o);
     }
     if (tok < R.T) {
-      const float f = R.normalize ? rcp_approx(total) * R.scale : R.scale;
+      const float f = R.normalize ? rcp_approx(total) : 1.f;  // (times the scale it could overflow)
       int32_t* ids = R.ids + tok * R.top_k;
       float* out = R.weights + tok * R.top_k;
       if (!all) {
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kBulkThreads) route_bulk_kernel(const __grid_c
         for (int u = 0; u < 2; ++u)
           if (2 * h + u < R.top_k) {
             ids[2 * h + u] = e2[u];
-            out[2 * h + u] = w2[u] * f;
+            out[2 * h + u] = w2[u] * f * R.scale;
           }
       }
     }

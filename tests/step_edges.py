@@ -195,8 +195,25 @@ def weights_sizes(be):
         check_sizes(be, [200], [70], 4, 2, 128, 1e4, 601, q_size, k_size)
 
 
+# ---------------------------------------------------------------- the router's weights of small scores
+def route_scales(be, tokens=(3, 2100)):
+    """Sigmoid scores of about e^-75, chosen by biases far enough apart, and scale factors of any size: the weights
+    are scale times the scores' shares (eight FP32 roundings, as in step_checks.check_route)."""
+    for T in tokens:
+        for E, k, groups, top in ((64, 8, 8, 4), (256, 8, 8, 4), (64, 3, 1, 1)):
+            x = (-75 + np.random.default_rng(E).standard_normal((T, E))).astype(np.float32)
+            b = (0.05 * np.random.default_rng(E + 1).permutation(E)).astype(np.float32)
+            for scale in (1e30, 1e10, 2.5, 1e-30):
+                for normalize in (True, False):
+                    ids, w = be.route(x, b, k, groups, top, False, normalize, scale)
+                    rid, rw = steps.route_grouped(x, b, k, groups, top, False, normalize, np.float32(scale).astype(np.float64))
+                    assert np.array_equal(ids, rid)
+                    close(w, rw, np.abs(rw) * 2.0 ** -20 + 2.0 ** -149, f"weights, {T} tokens, {E} experts, scale {scale}, normalised {normalize}")
+
+
 # Cases by name.
 CASES = {
+    "route_scales": route_scales,
     "weights_sizes": weights_sizes,
     "gradient_peaked": gradient_peaked,
     "gradient_levels": gradient_levels,

@@ -10,3 +10,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("name", sorted(step_edges.CASES))
 def test_edges(be, name):  # noqa: F811
     step_edges.CASES[name](be)
+
+
+def test_router_scales_of_many_tokens(be):  # noqa: F811
+    step_edges.route_scales(be, (30000,))  # the kernel of four threads per token

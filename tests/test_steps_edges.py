@@ -32,6 +32,14 @@ def test_edges(host_library, name):
     assert rc == 0, log
 
 
+def test_edges_with_few_sms(host_library):
+    """On one SM and three the router takes its kernel of four threads per token from a few hundred tokens on, and
+    CTAs walk several rows and tiles."""
+    for sms in (1, 3):
+        rc, log = run(host_library, ["gradient_places", "route_scales", "weights_sizes"], sms)
+        assert rc == 0, log
+
+
 def test_e4m3_codes_against_torch():
     """The tests' own rounding to E4M3."""
     import torch
