@@ -868,12 +868,21 @@ int launch_evict_c(ev::EvictParams& P, int dev, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? MIMO_OK : MIMO_ERR_CUDA;
 }
 
+// CTAs to a sequence: as many as its length pays for, where the sequences' clusters all run at once (14 of eight
+// CTAs, 32 of four and 74 of two fit the 148 SMs; a second round of them costs more than fewer CTAs).  Measured, us:
+//   64 x 8192 one CTA 11.7, two 11.9   16384: one 17.6, two 14.0, four 13.7   24576: two 17.8, four 15.4, eight 17.6
+//   65536: four 22.2, eight 20.3   131072: four 34.8, eight 26.3   64 x 24576: two 17.8, four 27.5, eight 71
+//   16 x 131072: four 34.7, eight 51.8   148 x 32768: one 30.1, two 39.9
 int launch_evict(ev::EvictParams& P, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MIMO_ERR_CUDA;
-  if (P.max_kv_len <= 2048) return launch_evict_c<1>(P, dev, stream);
-  if (P.max_kv_len <= 16384) return launch_evict_c<2>(P, dev, stream);
-  return launch_evict_c<ev::kMaxCluster>(P, dev, stream);
+  DeviceInfo* info = device_info(dev);
+  if (!info) return MIMO_ERR_CUDA;
+  const int64_t n = P.num_seqs, sms = info->sms;
+  if (P.max_kv_len > 65536 && 10 * n <= sms) return launch_evict_c<ev::kMaxCluster>(P, dev, stream);
+  if (P.max_kv_len > 16384 && 32 * n <= 7 * sms) return launch_evict_c<4>(P, dev, stream);
+  if (P.max_kv_len > 8192 && 2 * n <= sms) return launch_evict_c<2>(P, dev, stream);
+  return launch_evict_c<1>(P, dev, stream);
 }
 
 // ---------------------------------------------------------------- key weights

@@ -7,7 +7,7 @@ import numpy as np
 
 from oracle import steps
 from oracle.neighbors import bf16_bits_to_f64, e4m3_to_f64
-from step_checks import bits, close, step_batch, weights_tolerance
+from step_checks import bits, check_evict, close, step_batch, weights_tolerance
 
 
 # ---------------------------------------------------------------- RMS norm: the FP8 codes
@@ -211,8 +211,20 @@ def route_scales(be, tokens=(3, 2100)):
                     close(w, rw, np.abs(rw) * 2.0 ** -20 + 2.0 ** -149, f"weights, {T} tokens, {E} experts, scale {scale}, normalised {normalize}")
 
 
+# ---------------------------------------------------------------- eviction by every number of CTAs to a sequence
+def evict_clusters(be):
+    """One, two, four and eight CTAs to a sequence (by length; by number, where there are many), with and without
+    room for the weights in shared memory, and the same batch in several forms: the results agree bit for bit."""
+    for lens, budget in (([8192], 1000), ([8193, 3, 0, 600], 2000), ([16384], 16383), ([16385, 40], 5000), ([65536], 100),
+                         ([70001, 9], 30000), ([9000] + [5] * 80, 700), ([17000] + [3] * 40, 700), ([70000] + [1] * 15, 6000),
+                         ([50000] + [2] * 80, 49999)):
+        for kind in ("spread", "ties", "wild"):
+            check_evict(be, lens, budget, 3, 40, 700 + len(lens), kind)
+
+
 # Cases by name.
 CASES = {
+    "evict_clusters": evict_clusters,
     "route_scales": route_scales,
     "weights_sizes": weights_sizes,
     "gradient_peaked": gradient_peaked,
