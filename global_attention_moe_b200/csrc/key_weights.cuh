@@ -88,7 +88,6 @@ struct Params {
   int32_t splits;             // parts of the query tiles
   int32_t parts;              // partial rows to a KV head: 1, or two to a split
   int32_t ntile;              // query rows per tile (MMA N): multiple of 16, at most 128
-  int32_t contiguous;         // a CTA's units: a run (1) or every gridDim-th (0)
   float scale_log2;
   uint64_t wait_limit_ns;
   double theta[kRopeDims / 2];

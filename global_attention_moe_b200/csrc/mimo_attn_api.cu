@@ -951,7 +951,6 @@ int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const 
   P.splits = plan.splits;
   P.parts = plan.parts;
   P.ntile = plan.ntile;
-  P.contiguous = plan.contiguous ? 1 : 0;
   P.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDimQK)));
   P.wait_limit_ns = kDefaultWaitLimitNs;
   for (int i = 0; i < kRopeDims / 2; ++i) P.theta[i] = std::pow(rope_base, -2.0 * i / kRopeDims);
@@ -964,12 +963,12 @@ int launch_key_weights(const void* q, const void* kc, const int32_t* idx, const 
     if (!encode_2d(&tq, P.qs, 256, (uint64_t)d->total_q * P.hq, (uint32_t)P.ntile)) return MIMO_ERR_CUDA;
     const long long units = ((long long)d->total_kv / kw::kTile + d->num_seqs) * P.hkv * P.splits;
     // one CTA per SM; with runs of tiles (one query tile to a sequence) as many for each KV head
-    const unsigned grid = P.contiguous ? (unsigned)(P.hkv * std::max(1LL, std::min<long long>(units, info->sms) / P.hkv))
+    const unsigned grid = plan.contiguous ? (unsigned)(P.hkv * std::max(1LL, std::min<long long>(units, info->sms) / P.hkv))
                                        : (unsigned)std::min<long long>(units, info->sms);
     // K stages of 48 KB and Q tiles of ntile / 2 KB within 224 KB
-    if (P.contiguous && P.ntile <= 64)
+    if (plan.contiguous && P.ntile <= 64)
       kw::kw_main_kernel<4, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
-    else if (P.contiguous)
+    else if (plan.contiguous)
       kw::kw_main_kernel<3, 1><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);
     else
       kw::kw_main_kernel<2, 2><<<grid, kw::kThreads, kw::kSmemBytes, stream>>>(tq, P);

@@ -69,16 +69,13 @@ __device__ __forceinline__ void route_exact(const RouteParams& P, int64_t tok, i
   double sc[kMaxPerLane];
   if (P.softmax) {
     float mx = -INFINITY;
-    bool nan = false;
 #pragma unroll
     for (int m = 0; m < kMaxPerLane; ++m) {
       const float v = lane + 32 * m < P.E ? __ldg(x + lane + 32 * m) : -INFINITY;
       sc[m] = v;
-      nan |= v != v;
       mx = fmaxf(mx, v);
     }
     mx = warp_max(mx);
-    nan = __any_sync(0xffffffffu, nan);
     double sum = 0.0;
 #pragma unroll
     for (int m = 0; m < kMaxPerLane; ++m) {
