@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
       unpack8(hv[i], a);
       unpack8(rv[i], b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] += b[e];
+      for (int e = 0; e < 8; e += 2) {
+        const float2 h2 = fadd2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+        a[e] = h2.x, a[e + 1] = h2.y;
+      }
       hv[i] = pack8(a);
     }
   }
@@ -192,14 +195,17 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
       float w[8];
       load_w<WT>(P.w, v, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * w[e];
+      for (int e = 0; e < 8; e += 2) {  // (f rstd) w
+        const float2 y2 = fmul2(fmul2(make_float2(f[e], f[e + 1]), make_float2(rstd, rstd)), make_float2(w[e], w[e + 1]));
+        f[e] = y2.x, f[e + 1] = y2.y;
+      }
     }
     if (P.y != nullptr && in) reinterpret_cast<uint4*>(P.y + row * P.H)[v] = pack8(f);
     if (kFp8) {
       // the block's 16 vectors are in the 16 lanes of this half-warp (those past the row hold zeros)
       float a = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+      for (int e = 0; e < 8; e += 2) a = fmax3(a, fabsf(f[e]), fabsf(f[e + 1]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       const float scale = fmaxf(__fdiv_rn(a, kFp8Max), 0x1p-126f);  // a block of zeros: the smallest normal scale
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
         // (Markstein), so that they are the rounded y / scale.  With BF16 rows and weights 2 of 10000 lie on a midpoint
         // of two codes, where the reciprocal's rounding would decide.  Negated, so that zeros keep their sign; an
         // infinite scale takes no step (codes 0, and NaN where y is infinite).  A division for each: 82 us, for those
-        // near a midpoint 79 to 90, this 73 (16384 x 4096).
+        // near a midpoint 79 to 90, this, as the reciprocal alone, 73 (16384 x 4096).
         const float ninv = -1.f / scale, sc = scale < INFINITY ? scale : 0.f;
         uint32_t c[4];
 #pragma unroll
@@ -216,9 +222,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
           const float2 y2 = make_float2(f[2 * e], f[2 * e + 1]), ninv2 = make_float2(ninv, ninv);
           float2 q = fmul2(y2, ninv2);
           q = ffma2(ffma2(q, make_float2(sc, sc), y2), ninv2, q);
-          c[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) ^ 0x8080u;
+          c[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
         }
-        reinterpret_cast<uint2*>(P.codes + row * P.H)[v] = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        reinterpret_cast<uint2*>(P.codes + row * P.H)[v] =
+            make_uint2((c[0] | (c[1] << 16)) ^ 0x80808080u, (c[2] | (c[3] << 16)) ^ 0x80808080u);
         if ((v & 15) == 0) P.scale[row * blocks + (v >> 4)] = scale;
       }
     }
