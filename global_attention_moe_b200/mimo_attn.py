@@ -417,7 +417,8 @@ def _check(name, t, dtype, shape, dev):
 
 
 def _int32(*numbers):
-    """Of a larger number ctypes would pass the low 32 bits."""
+    """Of a larger number ctypes would pass the low 32 bits.  Called where the numbers' bits, joined by `or`, are not
+    all below 2^31 (which costs a call less than their maximum and minimum)."""
     if max(numbers) > 0x7FFFFFFF or min(numbers) < -0x80000000:
         raise ValueError(f"a size or choice beyond 32 bits among {numbers}")
 
@@ -512,7 +513,9 @@ def moe_route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, sc
     ids int32 [T, top_k], weights fp32 [T, top_k] (scale times the scores, normalised to sum to one first)."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
-    _int32(logits.shape[1], top_k, num_groups, top_groups, score)
+    T, E = logits.shape
+    if (E | top_k | num_groups | top_groups | score) >> 31:
+        _int32(E, top_k, num_groups, top_groups, score)
     dev = torch.cuda.current_device()
     _check("logits", logits, _F32, logits.shape, dev)
     if bias is not None:
@@ -520,7 +523,6 @@ def moe_route_grouped(logits, bias=None, top_k=8, num_groups=1, top_groups=1, sc
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_route_grouped(logits, bias, top_k, num_groups, top_groups, score, normalize, scale)
-    T, E = logits.shape
     w = logits.new_empty((T, top_k if top_k > 0 else 0))
     ids = torch.empty_like(w, dtype=_I32)
     st = LIB.mimo_moe_route_grouped(logits.data_ptr(), None if bias is None else bias.data_ptr(), T, E, top_k,
@@ -537,10 +539,11 @@ def moe_route_bwd(logits, ids, dweights, score=ROUTE_SIGMOID, normalize=True, sc
     [0, E) is an empty place."""
     if logits.dim() != 2 or ids.dim() != 2:
         raise ValueError(f"logits and ids must be [tokens, ...], got {tuple(logits.shape)} and {tuple(ids.shape)}")
-    _int32(logits.shape[1], ids.shape[1], score)
-    dev = torch.cuda.current_device()
     T, E = logits.shape
     k = ids.shape[1]
+    if (E | k | score) >> 31:
+        _int32(E, k, score)
+    dev = torch.cuda.current_device()
     _check("logits", logits, _F32, logits.shape, dev)
     _check("ids", ids, _I32, (T, k), dev)
     _check("dweights", dweights, _F32, (T, k), dev)
@@ -566,7 +569,8 @@ def decode_key_weights(q, k_cache, kv_indices, kv_indptr, cu_q, lse, max_q_len, 
     Tq, hq, dqk = q.shape
     rows, hkv, _ = k_cache.shape
     total, B1 = kv_indices.shape[0], cu_q.shape[0]
-    _int32(Tq, rows, total, B1, max_q_len, max_kv_len, layer_kind, window, rope_dims)
+    if (Tq | rows | total | B1 | max_q_len | max_kv_len | layer_kind | window + 1 | rope_dims) >> 31:
+        _int32(Tq, rows, total, B1, max_q_len, max_kv_len, layer_kind, window, rope_dims)
     dev = torch.cuda.current_device()
     _check("q", q, _BF16, q.shape, dev)
     _check("k_cache", k_cache, _BF16, (rows, hkv, dqk), dev)
@@ -604,7 +608,8 @@ def kv_evict(weights, kv_indices, kv_indptr, max_kv_len, budget, keep_first=0, k
     if kv_indices.dim() != 1 or kv_indptr.dim() != 1:
         raise ValueError(f"the index lists must be flat, got {tuple(kv_indices.shape)} and {tuple(kv_indptr.shape)}")
     total, B1 = kv_indices.shape[0], kv_indptr.shape[0]
-    _int32(total, B1, max_kv_len)
+    if (total | B1 | max_kv_len) >> 31:
+        _int32(total, B1, max_kv_len)
     dev = torch.cuda.current_device()
     _check("weights", weights, _F32, (total,), dev)
     _check("kv_indices", kv_indices, _I32, (total,), dev)
