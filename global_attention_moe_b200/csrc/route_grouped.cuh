@@ -63,6 +63,14 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// e^(x - m), with the difference's rounding (which alone puts it off by |x - m| 2^-24) made good; m finite.
+__device__ __forceinline__ float exp_diff(float x, float m) {
+  const float t = x - m, e = expf(t);
+  if (!(t > -104.f)) return e;  // 0, or NaN
+  const float b = t - x, rest = (x - (t - b)) - (m + b);
+  return fmaf(e, rest, e);
+}
+
 // The definition for one token, by one warp: lane holds experts lane + 32 m; s_key: E floats of the warp's.
 __device__ __forceinline__ void route_exact(const RouteParams& P, int64_t tok, int lane, float* s_key) {
   const float* x = P.logits + tok * P.E;
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) route_fast_kernel(co
       }
       if (__all_sync(0xffffffffu, sure)) {
         float s = 0.f;
-        if (lane < R.top_k) s = kSoftmax ? expf(x - mx) * inv : rcp_approx(1.f + expf(-x));
+        if (lane < R.top_k) s = kSoftmax ? exp_diff(x, mx) * inv : rcp_approx(1.f + expf(-x));
         if (R.normalize) {
           float total = s;
 #pragma unroll
@@ -710,7 +718,7 @@ __global__ void __launch_bounds__(kBulkThreads) route_bulk_kernel(const __grid_c
       if (2 * h + u < R.top_k && sure && tok < R.T) {
         const float x = __ldg(R.logits + tok * R.E + e2[u]);
         sure = x - mx > -80.f;  // a score that FP32 holds
-        w2[u] = kSoftmax ? expf(x - mx) * inv : rcp_approx(1.f + expf(-x));
+        w2[u] = kSoftmax ? exp_diff(x, mx) * inv : rcp_approx(1.f + expf(-x));
       }
     }
     float total = w2[0] + w2[1];
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_sparse_kernel(const __grid
       const float diff = (g - __shfl_sync(0xffffffffu, g, D)) + (rest - __shfl_sync(0xffffffffu, rest, D));
       const float dev = has ? diff * P.scale : 0.f;
       const float base = P.softmax ? mx : fminf(mx, 0.f);
-      float s = !P.softmax && x >= 0.f ? r : base == 0.f ? e * r : expf(x - base) * r;
+      float s = !P.softmax && x >= 0.f ? r : base == 0.f ? e * r : exp_diff(x, base) * r;
       s = has && mx > -INFINITY ? s * count : 0.f;
       if (has && x != x) s = x;
       const float S = sum(s);
@@ -935,7 +943,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_dense_kernel(const __grid_
         v[m] = lane + 32 * m < P.E ? expf(v[m] - mx) : 0.f;
         U += (mine >> m) & 1u ? 0.f : v[m];
       }
-    const float s = has ? expf(xj - mx) : 0.f;
+    const float s = has ? exp_diff(xj, mx) : 0.f;
     float C = s, gm = g * s, dm = has ? dev * s : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

@@ -222,8 +222,26 @@ def evict_clusters(be):
             check_evict(be, lens, budget, 3, 40, 700 + len(lens), kind)
 
 
+def route_low(be, tokens=(3, 2100)):
+    """Softmax scores far below the largest, chosen by their biases: a weight is off by the roundings of one
+    exponential, its sum and a quotient (2^-20), not by that of the difference x - max, which grows with it (half of
+    2^-17 at 70); weights that keep the softmax's sum carry its approximate exponentials too (2^-19)."""
+    for T in tokens:
+        for E, k, groups, top in ((64, 8, 8, 4), (128, 8, 1, 1), (64, 3, 1, 1)):
+            rng = np.random.default_rng(E + T)
+            x = rng.uniform(-75, -20, (T, E)).astype(np.float32)
+            x[np.arange(T), rng.integers(0, E, T)] = rng.uniform(0, 3, T).astype(np.float32)
+            b = (3.0 * rng.permutation(E)).astype(np.float32)
+            for normalize, tol in ((True, 2.0 ** -20), (False, 2.0 ** -19)):
+                ids, w = be.route(x, b, k, groups, top, True, normalize, 2.5)
+                rid, rw = steps.route_grouped(x, b, k, groups, top, True, normalize, 2.5)
+                assert np.array_equal(ids, rid)
+                close(w, rw, np.abs(rw) * tol + 2.0 ** -149, f"weights, {T} tokens, {E} experts, normalised {normalize}")
+
+
 # Cases by name.
 CASES = {
+    "route_low": route_low,
     "evict_clusters": evict_clusters,
     "route_scales": route_scales,
     "weights_sizes": weights_sizes,

@@ -14,3 +14,7 @@ def test_edges(be, name):  # noqa: F811
 
 def test_router_scales_of_many_tokens(be):  # noqa: F811
     step_edges.route_scales(be, (30000,))  # the kernel of four threads per token
+
+
+def test_router_low_scores_of_many_tokens(be):  # noqa: F811
+    step_edges.route_low(be, (30000,))

@@ -36,7 +36,7 @@ def test_edges_with_few_sms(host_library):
     """On one SM and three the router takes its kernel of four threads per token from a few hundred tokens on, and
     CTAs walk several rows and tiles."""
     for sms in (1, 3):
-        rc, log = run(host_library, ["gradient_places", "route_scales", "weights_sizes"], sms)
+        rc, log = run(host_library, ["gradient_places", "route_low", "route_scales", "weights_sizes"], sms)
         assert rc == 0, log
 
 
