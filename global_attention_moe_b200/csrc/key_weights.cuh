@@ -44,9 +44,10 @@
 // while the keys of its sequence stream through KS stages; with more (chunked prefill, QS = 2) a key tile stays
 // in TMEM while the query tiles stream through two Q stages.
 //
-// 64 sequences of 8 tokens on 1024 to 8192 keys (470 MB of rows, 59 us of three-product MMAs): 131 us, the
-// gather and the sums' exponentials about level; a chunk of 300 tokens on 5000 keys: 88 us.  The role loops are
-// kept short: unrolled further, their instructions no longer fit the SM's cache and the decode case took 228 us.
+// 64 sequences of 8 tokens on 1024 to 8192 keys (470 MB of rows, 59 us of three-product MMAs): 134 us at 1965 MHz,
+// 157 to 161 where the power cap holds the clock at 1590, the gather and the sums' exponentials about level; a chunk
+// of 300 tokens on 5000 keys: 84 to 88 us.  The role loops are kept short: unrolled further, their instructions no
+// longer fit the SM's cache and the decode case took 228 us.
 #pragma once
 
 #include "attn_decode.cuh"

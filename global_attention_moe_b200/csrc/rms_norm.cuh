@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rms_norm_kernel(const _
       const float scale = fmaxf(__fdiv_rn(a, kFp8Max), 0x1p-126f);  // a block of zeros: the smallest normal scale
       if (in) {
         // The quotients, negated: q = y (1 / scale) and one step with the remainder y - q scale, which is exact
-        // (Markstein), so that they are the rounded y / scale.  With BF16 rows and weights 2 of 10000 lie on a midpoint
-        // of two codes, where the reciprocal's rounding would decide.  Negated, so that zeros keep their sign; an
-        // infinite scale takes no step (codes 0, and NaN where y is infinite).  A division for each: 82 us, for those
-        // near a midpoint 79 to 90, this, as the reciprocal alone, 73 (16384 x 4096).
+        // (Markstein), so that they are the rounded y / scale.  With BF16 rows and weights 2 to 4 of 10000 lie on a
+        // midpoint of two codes, where the reciprocal's rounding would decide.  Negated, so that zeros keep their
+        // sign; an infinite scale takes no step (codes 0, and NaN where y is infinite).  A division for each: 82 us,
+        // for those near a midpoint 79 to 90, this, as the reciprocal alone, 73 (16384 x 4096).
         const float ninv = -1.f / scale, sc = scale < INFINITY ? scale : 0.f;
         uint32_t c[4];
 #pragma unroll

@@ -260,7 +260,7 @@ CASES = {
                                for kind in ("ties", "near", "flat", "far", "masked")
                                for E, groups, top, softmax, bias in ((256, 8, 4, False, True), (256, 1, 1, True, False),
                                                                      (128, 4, 2, False, False), (160, 1, 1, True, True))],
-    # enough tokens for the kernel of one thread per token on an SM or two (and a ragged last tile)
+    # enough tokens for the kernel of four threads per token on an SM or two (and a ragged last tile)
     "route_many": lambda be: [check_route(be, T, E, k, groups, top, softmax, normalize, bias, 75 + E, kind, 2.5)
                               for T, E, k, groups, top, softmax, normalize, bias, kind in (
                                   (1111, 256, 8, 8, 4, False, True, True, "normal"), (1050, 256, 8, 1, 1, True, True, False, "normal"),
