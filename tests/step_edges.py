@@ -50,6 +50,35 @@ def fp8_codes(be):
         assert not off.any(), f"{off.sum()} of {off.size} codes of {H} columns, first at {tuple(np.argwhere(off)[0])}"
 
 
+def fp8_extremes(be):
+    """The same at the ends of FP32: blocks of zeros, of subnormals, of values near 2^-120 and near the largest, and
+    blocks with an infinite weight (scale infinite: codes 0, NaN where y is infinite)."""
+    rng = np.random.default_rng(8)
+    H = 128 * 6
+    w = rng.standard_normal(H)
+    for b, size in enumerate((0.0, 2.0 ** -140, 2.0 ** -118, 2.0 ** 126, 1.0, 2.0 ** -126)):
+        w[128 * b:128 * b + 128] *= size
+    w = w.astype(np.float32)
+    w = np.where(np.isfinite(w), w, np.float32(3e38))
+    w[128 * 4 + 9], w[128 * 4 + 40] = np.inf, -0.0
+    sign = rng.choice([-1.0, 1.0], (2, H))
+    got = be.rms_norm(bits(sign), w, None, 1e-18, y=False, fp8=True)
+    y = (sign * w).astype(np.float32)
+    scale = np.maximum(np.abs(y).reshape(2, -1, 128).max(-1) / np.float32(448.0), np.float32(2.0 ** -126)).astype(np.float32)
+    assert np.array_equal(got["scale"], scale)
+    with np.errstate(invalid="ignore"):
+        q = y / np.repeat(scale, 128, -1)
+    nan = np.isnan(q)
+    assert nan.sum() == 2 and np.all((got["codes"][nan] & 0x7F) == 0x7F)
+    # below about 2^-100 the remainder has no room: codes may be the neighbour's at a midpoint
+    exact = np.repeat((scale >= 2.0 ** -100), 128, -1) & ~nan
+    want = e4m3_codes(np.where(nan, 0, q))
+    assert np.array_equal(got["codes"][exact], want[exact])
+    near = ~exact & ~nan
+    v = e4m3_to_f64(got["codes"][near])
+    assert np.all(np.abs(v - q[near]) <= np.abs(q[near]) * 2.0 ** -4 * (1 + 2.0 ** -20) + 2.0 ** -10 * (1 + 2.0 ** -20))
+
+
 # ---------------------------------------------------------------- the router's gradient where one expert dominates
 def route_bwd_terms(x, ids, g, softmax, normalize, scale):
     """(dlogits, tolerance) of one token in FP64, from differences of the gradients g, so that nothing is lost where
@@ -280,4 +309,5 @@ CASES = {
     "gradient_alike": gradient_alike,
     "gradient_places": gradient_places,
     "fp8_codes": fp8_codes,
+    "fp8_extremes": fp8_extremes,
 }
