@@ -14,6 +14,7 @@
 // exponents from about 1 down, and queries of 3000 with keys of 3e-4 were off by 1.5e-5).  Three products hi hi +
 // 2^-11 (hi lo + lo hi) take the place of one, the last two first: the MMA that starts hi hi takes the accumulator
 // times 2^-11.  The pass-through dims are exact in BF16.  Rotation angles come from FP64-reduced positions.
+// Exponentials are ex2.approx (2 ulp); sums are FP32, four chains to a key and part.
 //
 // Three launches:
 //   1. kw_prep_kernel: Q rotated and split once, into rows of 256 16-bit values (hi 64, lo 64, pass 128)

@@ -19,7 +19,9 @@
 //      comparing with each; lanes of the groups that are not kept drop out;
 //   3. top_k times, the warp's largest first key (one integer reduction) is taken from its lane;
 //   4. where every two neighbours of the k + 1 largest differ by more than twice the error bound, their
-//      order is that of the exact keys: the chosen experts' scores are formed in FP32 and written.
+//      order is that of the exact keys: the chosen experts' scores are formed in FP32 and written (exponentials
+//      and reciprocals of 1 to 2 ulp: weights within 2^-19, where FP64 would cost as much as the choice; only the
+//      order needs more).
 // Other tokens are marked in ids and taken up after the loop, whose registers then hold no call: the experts
 // within the bound of the k-th key (at most 32) take their exact keys in FP64 and are ranked; and where that
 // does not decide either (group scores within the bound, more than 32 candidates, keys that are NaN,
